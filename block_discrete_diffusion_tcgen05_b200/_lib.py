@@ -15,7 +15,8 @@ DEBUG_LIBRARY = PKG / "libe2d2_attn_debug.so"
 # Names and values of include/e2d2_attn.h's e2d2_status.
 STATUS = {0: "E2D2_OK", 1: "E2D2_ERR_INVALID_ARG", 2: "E2D2_ERR_UNSUPPORTED", 3: "E2D2_ERR_SHAPE",
           4: "E2D2_ERR_ALIGNMENT", 5: "E2D2_ERR_CAPACITY", 6: "E2D2_ERR_WORKSPACE",
-          7: "E2D2_ERR_CUDA", 8: "E2D2_ERR_TIMEOUT", 9: "E2D2_ERR_DEVICE_CHECK"}
+          7: "E2D2_ERR_CUDA", 8: "E2D2_ERR_TIMEOUT", 9: "E2D2_ERR_DEVICE_CHECK",
+          10: "E2D2_ERR_PAGE"}
 
 EXPORTS = ("e2d2_attn_encoder_blockcausal", "e2d2_attn_decoder_train",
            "e2d2_attn_decoder_sample_workspace", "e2d2_attn_decoder_sample",
@@ -24,7 +25,10 @@ EXPORTS = ("e2d2_attn_encoder_blockcausal", "e2d2_attn_decoder_train",
            "e2d2_attn_train_backward_workspace", "e2d2_attn_encoder_backward",
            "e2d2_attn_decoder_train_backward", "e2d2_attn_decoder_sample_plan", "e2d2_attn_train_order",
            "e2d2_attn_decoder_sample_ragged", "e2d2_attn_decoder_sample_ragged_plan",
-           "e2d2_debug_set_wait_test", "e2d2_kv_cache_append_ragged")
+           "e2d2_debug_set_wait_test", "e2d2_kv_cache_append_ragged",
+           "e2d2_attn_decoder_sample_paged_workspace", "e2d2_attn_decoder_sample_paged",
+           "e2d2_kv_cache_append_paged", "e2d2_kv_cache_weigh", "e2d2_kv_cache_evict_workspace",
+           "e2d2_kv_cache_evict")
 
 # E2D2_SAMPLE_NOALLOC_MAX_BYTES of include/e2d2_attn.h
 SAMPLE_NOALLOC_MAX_BYTES = 32 << 20
@@ -35,6 +39,13 @@ class Dims(ctypes.Structure):
 
     _fields_ = [("batch", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Pages(ctypes.Structure):
+    """e2d2_pages."""
+
+    _fields_ = [("num_pages", ctypes.c_int), ("page_rows", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_table", ctypes.c_void_p)]
 
 
 class SamplePlan(ctypes.Structure):
@@ -106,6 +117,18 @@ def load(path: Path | str | None = None):
     lib.e2d2_attn_decoder_sample_ragged_plan.argtypes = [Dims, ci, ctypes.POINTER(ctypes.c_int), ci, ci,
                                                          ctypes.POINTER(RaggedPlan)]
     lib.e2d2_attn_decoder_sample_ragged_plan.restype = ctypes.c_int
+    sz = ctypes.c_size_t
+    lib.e2d2_attn_decoder_sample_paged_workspace.argtypes = [Dims, ci]
+    lib.e2d2_attn_decoder_sample_paged_workspace.restype = sz
+    lib.e2d2_attn_decoder_sample_paged.argtypes = [vp, vp, vp, Pages, vp, vp, vp, vp, fp, Dims, ci, vp, sz, st]
+    lib.e2d2_kv_cache_append_paged.argtypes = [vp, vp, Pages, vp, vp, vp, ci, fp, vp, vp, Dims, st]
+    lib.e2d2_kv_cache_weigh.argtypes = [vp, vp, Pages, vp, fp, fp, fp, Dims, ci, st]
+    lib.e2d2_kv_cache_evict_workspace.argtypes = [Dims, Pages]
+    lib.e2d2_kv_cache_evict_workspace.restype = sz
+    lib.e2d2_kv_cache_evict.argtypes = [vp, vp, Pages, vp, fp, vp, vp, ci, ci, fp, vp, vp, Dims, vp, sz, st]
+    for name in ("e2d2_attn_decoder_sample_paged", "e2d2_kv_cache_append_paged", "e2d2_kv_cache_weigh",
+                 "e2d2_kv_cache_evict"):
+        getattr(lib, name).restype = ci
     lib.e2d2_status_string.argtypes = [ci]
     lib.e2d2_status_string.restype = ctypes.c_char_p
     lib.e2d2_last_device_error.argtypes = [st]

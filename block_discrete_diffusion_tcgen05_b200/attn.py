@@ -369,6 +369,181 @@ def kv_cache_append_ragged(k_cache, v_cache, P, k_new, v_new):
     _lib.check(st, "e2d2_kv_cache_append_ragged")
 
 
+def _pages(k_pages: torch.Tensor, page_table, batch: int):
+    """The e2d2_pages of a pool [num_pages, Hkv, page_rows, d] and its table (CUDA int32
+    [batch, max_pages]; None: contiguous caches, one page per entry), and the row capacity."""
+    num_pages, page_rows = k_pages.shape[0], k_pages.shape[2]
+    if page_table is None:
+        if num_pages != batch:
+            raise ValueError("without a page table the caches must be [B, Hkv, capacity, d]")
+        return _lib.Pages(num_pages, page_rows, 1, None), page_rows
+    _need(page_table, "page_table", dtype=torch.int32, ndim=2)
+    if page_table.shape[0] != batch:
+        raise ValueError("page_table must be [B, max_pages]")
+    max_pages = page_table.shape[1]
+    return _lib.Pages(num_pages, page_rows, max_pages, page_table.data_ptr()), max_pages * page_rows
+
+
+def _need_ints(t, name: str, batch: int):
+    _need(t, name, dtype=torch.int32, ndim=1)
+    if t.shape[0] != batch:
+        raise ValueError(f"{name} must be [B]")
+
+
+def _need_rows(t, name: str, shape, dtype):
+    _need(t, name, dtype=dtype, ndim=3)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [B, Hkv, row capacity] = {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def sample_paged_workspace_bytes(batch, q_heads, kv_heads, head_dim, S) -> int:
+    """Bytes of workspace a paged sampling call needs (no GPU needed)."""
+    lib = _lib.load()
+    return int(lib.e2d2_attn_decoder_sample_paged_workspace(_dims(batch, q_heads, kv_heads, head_dim, None), S))
+
+
+@_device_guard
+def sample_paged_workspace(q_blk: torch.Tensor, k_pages: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for decoder_sample_paged with these shapes."""
+    B, Hq, S, d = q_blk.shape
+    n = sample_paged_workspace_bytes(B, Hq, k_pages.shape[1], d, S)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=q_blk.device)
+
+
+@_device_guard
+def decoder_sample_paged(q_blk, k_pages, v_pages, page_table, P, k_blk=None, v_blk=None, workspace=None, scale=None,
+                         out=None, lse=True):
+    """Sampling step over a paged cache (S = 1: one new token): q_blk [B,Hq,S,d]; pools k_pages/v_pages
+    [num_pages,Hkv,page_rows,d]; page_table CUDA int32 [B,max_pages] or None (contiguous caches
+    [B,Hkv,capacity,d]); P CUDA int32 [B].  Entry b's queries see its first P[b] rows and, if given, the
+    block's own k_blk/v_blk [B,Hkv,S,d].  Returns (out, lse); a row that sees nothing: zeros and -inf."""
+    lib = _lib.load()
+    for t, n in ((q_blk, "q_blk"), (k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need(t, n)
+    B, Hq, S, d = q_blk.shape
+    Hkv = k_pages.shape[1]
+    if k_pages.shape[3] != d or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_rows, d] matching q_blk")
+    pages, _ = _pages(k_pages, page_table, B)
+    _need_ints(P, "P", B)
+    if (k_blk is None) != (v_blk is None):
+        raise ValueError("k_blk and v_blk must both be given or both be None")
+    if k_blk is not None:
+        _need(k_blk, "k_blk")
+        _need(v_blk, "v_blk")
+        if k_blk.shape != (B, Hkv, S, d) or v_blk.shape != k_blk.shape:
+            raise ValueError("k_blk/v_blk must be [B, Hkv, S, d]")
+    ws = sample_paged_workspace(q_blk, k_pages) if workspace is None else _need_workspace(workspace)
+    out = _out_tensor(out, q_blk)
+    lse_t = _lse_tensor(lse, (B, Hq, S), q_blk.device)
+    st = lib.e2d2_attn_decoder_sample_paged(q_blk.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages,
+                                            P.data_ptr(), _ptr(k_blk), _ptr(v_blk), out.data_ptr(), _ptr(lse_t),
+                                            _dims(B, Hq, Hkv, d, scale), S, ws.data_ptr(),
+                                            ws.numel() * ws.element_size(), _stream(q_blk))
+    _lib.check(st, "e2d2_attn_decoder_sample_paged")
+    return out, lse_t
+
+
+@_device_guard
+def kv_cache_append_paged(k_pages, v_pages, page_table, P, k_new, v_new, weight=None, pos=None, tokens=None):
+    """Writes k_new/v_new [B,Hkv,S_new,d] into rows P[b]..P[b]+S_new-1 of entry b (P is not advanced).
+    With weight (fp32 [B,Hkv,row capacity]), pos (int32, the same shape) and tokens (int32 [B]: tokens seen
+    before the block), the new rows' weight becomes 0 and their position tokens[b] + i."""
+    lib = _lib.load()
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_new, "k_new"), (v_new, "v_new")):
+        _need(t, n)
+    B, Hkv, S_new, d = k_new.shape
+    if k_pages.shape[1] != Hkv or k_pages.shape[3] != d or v_pages.shape != k_pages.shape or v_new.shape != k_new.shape:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_rows, d], k_new/v_new [B, Hkv, S_new, d]")
+    pages, cap = _pages(k_pages, page_table, B)
+    _need_ints(P, "P", B)
+    if len({weight is None, pos is None, tokens is None}) != 1:
+        raise ValueError("weight, pos and tokens must be given together")
+    if weight is not None:
+        _need_rows(weight, "weight", (B, Hkv, cap), torch.float32)
+        _need_rows(pos, "pos", (B, Hkv, cap), torch.int32)
+        _need_ints(tokens, "tokens", B)
+    st = lib.e2d2_kv_cache_append_paged(k_pages.data_ptr(), v_pages.data_ptr(), pages, P.data_ptr(), k_new.data_ptr(),
+                                        v_new.data_ptr(), S_new, _ptr(weight), _ptr(pos), _ptr(tokens),
+                                        _dims(B, Hkv, Hkv, d, None), _stream(k_pages))
+    _lib.check(st, "e2d2_kv_cache_append_paged")
+
+
+@_device_guard
+def kv_cache_weigh(q, k_pages, page_table, P, lse, weight, out=None, scale=None):
+    """Accumulated attention weight: returns out [B,Hkv,row capacity] (default: weight itself, in place) with
+    out[b,h,j] = weight[b,h,j] + sum of exp(scale q_i.k_j - lse_i) over the query rows that read head h, for
+    j < P[b]; other rows are not written.  q [B,Hq,S,d] and lse [B,Hq,S] (fp32) of an attention call."""
+    lib = _lib.load()
+    _need(q, "q")
+    _need(k_pages, "k_pages")
+    B, Hq, S, d = q.shape
+    Hkv = k_pages.shape[1]
+    if k_pages.shape[3] != d:
+        raise ValueError("k_pages must be [num_pages, Hkv, page_rows, d] matching q")
+    pages, cap = _pages(k_pages, page_table, B)
+    _need_ints(P, "P", B)
+    _need(lse, "lse", dtype=torch.float32, ndim=3)
+    if lse.shape != (B, Hq, S):
+        raise ValueError("lse must be [B, Hq, S]")
+    _need_rows(weight, "weight", (B, Hkv, cap), torch.float32)
+    if out is None:
+        out = weight
+    else:
+        _need_rows(out, "out", (B, Hkv, cap), torch.float32)
+    st = lib.e2d2_kv_cache_weigh(q.data_ptr(), k_pages.data_ptr(), pages, P.data_ptr(), lse.data_ptr(),
+                                 weight.data_ptr(), out.data_ptr(), _dims(B, Hq, Hkv, d, scale), S, _stream(q))
+    _lib.check(st, "e2d2_kv_cache_weigh")
+    return out
+
+
+def evict_workspace_bytes(batch, kv_heads, row_capacity) -> int:
+    """Bytes of workspace an eviction needs (no GPU needed)."""
+    lib = _lib.load()
+    return int(lib.e2d2_kv_cache_evict_workspace(_dims(batch, kv_heads, kv_heads, 64, None),
+                                                 _lib.Pages(batch, row_capacity, 1, None)))
+
+
+@_device_guard
+def evict_workspace(weight: torch.Tensor) -> torch.Tensor:
+    """A workspace for kv_cache_evict with weight [B,Hkv,row capacity]."""
+    B, Hkv, cap = weight.shape
+    return torch.empty(max(evict_workspace_bytes(B, Hkv, cap), 16), dtype=torch.uint8, device=weight.device)
+
+
+@_device_guard
+def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: int, recent: int = 0, weight_out=None,
+                   pos_out=None, P_out=None, workspace=None):
+    """Evicts rows until every entry holds at most `keep`: the rows at positions >= tokens[b] - recent stay,
+    then the heaviest (ties: the lowest row).  Kept rows at or past `keep` move, K, V, weight and position,
+    into the rows below it that are not kept.  weight (fp32), pos (int32) [B,Hkv,row capacity]; P, tokens
+    int32 [B].  weight_out, pos_out, P_out default to weight, pos and P, in place.  Returns P_out."""
+    lib = _lib.load()
+    _need(k_pages, "k_pages")
+    _need(v_pages, "v_pages")
+    _need(weight, "weight", dtype=torch.float32, ndim=3)
+    B, Hkv, d = weight.shape[0], k_pages.shape[1], k_pages.shape[3]
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    pages, cap = _pages(k_pages, page_table, B)
+    _need_ints(P, "P", B)
+    _need_ints(tokens, "tokens", B)
+    weight_out = weight if weight_out is None else weight_out
+    pos_out = pos if pos_out is None else pos_out
+    P_out = P if P_out is None else P_out
+    for t, n, dt in ((weight, "weight", torch.float32), (weight_out, "weight_out", torch.float32),
+                     (pos, "pos", torch.int32), (pos_out, "pos_out", torch.int32)):
+        _need_rows(t, n, (B, Hkv, cap), dt)
+    _need_ints(P_out, "P_out", B)
+    ws = evict_workspace(weight) if workspace is None else _need_workspace(workspace)
+    st = lib.e2d2_kv_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), pages, P.data_ptr(), weight.data_ptr(),
+                                 pos.data_ptr(), tokens.data_ptr(), int(keep), int(recent), weight_out.data_ptr(),
+                                 pos_out.data_ptr(), P_out.data_ptr(), _dims(B, Hkv, Hkv, d, None), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _stream(k_pages))
+    _lib.check(st, "e2d2_kv_cache_evict")
+    return P_out
+
+
 def last_device_error(device=None) -> int:
     lib = _lib.load()
     return int(lib.e2d2_last_device_error(torch.cuda.current_stream(device).cuda_stream))

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -19,6 +20,9 @@
 #include "fmha_keyrow_sm100.cuh"
 #include "fmha_sm100.cuh"
 #include "kv_append.cuh"
+#include "kv_evict.cuh"
+#include "kv_paged.cuh"
+#include "paged_attn.cuh"
 
 namespace e2d2 {
 
@@ -670,6 +674,7 @@ const char* e2d2_status_string(e2d2_status s) {
         case E2D2_ERR_CUDA: return "E2D2_ERR_CUDA";
         case E2D2_ERR_TIMEOUT: return "E2D2_ERR_TIMEOUT";
         case E2D2_ERR_DEVICE_CHECK: return "E2D2_ERR_DEVICE_CHECK";
+        case E2D2_ERR_PAGE: return "E2D2_ERR_PAGE";
     }
     return "E2D2_ERR_UNKNOWN";
 }
@@ -898,7 +903,8 @@ e2d2_status e2d2_last_device_error(cudaStream_t stream) {
     if (word != 0) {
         const unsigned int zero = 0;
         if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) return E2D2_ERR_CUDA;
-        return (word & kErrDeviceCheck) ? E2D2_ERR_DEVICE_CHECK : E2D2_ERR_TIMEOUT;
+        if (word & kErrDeviceCheck) return E2D2_ERR_DEVICE_CHECK;
+        return (word & kErrWaitTimeout) ? E2D2_ERR_TIMEOUT : E2D2_ERR_PAGE;
     }
     return E2D2_OK;
 }
@@ -912,6 +918,261 @@ e2d2_status e2d2_debug_set_wait_test(unsigned long long wait_limit_ns, unsigned 
         cudaMemcpyToSymbol(g_test_producer_delay_ns, &producer_delay_ns, sizeof(producer_delay_ns)) != cudaSuccess)
         return E2D2_ERR_CUDA;
     return E2D2_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Paged KV cache: sampling step, append, accumulated attention weight, eviction.
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+// The pool and its table: sizes positive, a table's pages whole groups of 16 rows, no table for a pool of
+// one page per entry; everything that the kernels index stays inside 32 bits per entry and 64 overall.
+e2d2_status check_pages(const e2d2_pages& pg, const e2d2_dims& dims) {
+    if (pg.num_pages <= 0 || pg.page_rows <= 0 || pg.max_pages <= 0) return E2D2_ERR_INVALID_ARG;
+    if (pg.page_table == nullptr) {
+        if (pg.max_pages != 1 || pg.num_pages != dims.batch) return E2D2_ERR_INVALID_ARG;
+    } else if (pg.page_rows % 16 != 0) {
+        return E2D2_ERR_UNSUPPORTED;
+    }
+    if (dims.batch > kPagedMaxBatch) return E2D2_ERR_SHAPE;
+    const long long cap = static_cast<long long>(pg.max_pages) * pg.page_rows;
+    if (cap > kMaxI32 / 2 || static_cast<long long>(pg.num_pages) * dims.kv_heads > kMaxI32 ||
+        static_cast<long long>(dims.batch) * dims.kv_heads > 65535)
+        return E2D2_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(pg.page_table) & 3u) return E2D2_ERR_ALIGNMENT;
+    return E2D2_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+PageView page_view(const e2d2_pages& pg, const e2d2_dims& dims, const DeviceInfo* di) {
+    PageView v;
+    v.table = pg.page_table;
+    v.num_pages = pg.num_pages;
+    v.page_rows = pg.page_rows;
+    v.max_pages = pg.max_pages;
+    v.kv_heads = dims.kv_heads;
+    v.err = di->err;
+    return v;
+}
+
+long long row_capacity(const e2d2_pages& pg) { return static_cast<long long>(pg.max_pages) * pg.page_rows; }
+
+// Blocks of 256 threads for `items` thread-steps, at most eight per SM.
+unsigned copy_blocks(long long items, const DeviceInfo* di) {
+    long long blocks = (items + 255) / 256;
+    const long long cap = static_cast<long long>(di->sms) * 8;
+    if (blocks > cap) blocks = cap;
+    return static_cast<unsigned>(blocks < 1 ? 1 : blocks);
+}
+
+template <int D>
+e2d2_status launch_paged_attn(const PagedAttnParams& a, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(a.batch) * a.q_heads * a.S;
+    return launch_pdl(paged_attn_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, a) == cudaSuccess
+               ? E2D2_OK
+               : E2D2_ERR_CUDA;
+}
+
+template <int D>
+e2d2_status launch_weigh(const WeighParams& a, int capacity, const DeviceInfo* di, cudaStream_t stream) {
+    const unsigned units = static_cast<unsigned>(a.batch) * a.pages.kv_heads;
+    unsigned x = (di->sms * 8 + units - 1) / units;
+    const unsigned most = static_cast<unsigned>((capacity + 7) / 8);
+    if (x > most) x = most;
+    return launch_pdl(kv_weigh_kernel<D>, dim3(x, units), dim3(256), 0, stream, a) == cudaSuccess ? E2D2_OK
+                                                                                                  : E2D2_ERR_CUDA;
+}
+
+size_t paged_workspace_bytes(const e2d2_dims& dims, int S) {
+    (void)dims;
+    (void)S;
+    return 1024;
+}
+
+// Rows that one list of an eviction can hold, rounded to whole 16 bytes.
+long long evict_list_rows(const e2d2_pages& pg) { return (row_capacity(pg) / 2 + 4) / 4 * 4; }
+
+size_t evict_workspace_bytes(const e2d2_dims& dims, const e2d2_pages& pg) {
+    return static_cast<size_t>(dims.batch) * dims.kv_heads * (4 + 2 * evict_list_rows(pg)) * sizeof(int);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t e2d2_attn_decoder_sample_paged_workspace(e2d2_dims dims, int S) {
+    if (check_dims(dims) != E2D2_OK || S <= 0) return 0;
+    return paged_workspace_bytes(dims, S);
+}
+
+e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_pages, const void* v_pages,
+                                           e2d2_pages pages, const int* P_dev, const void* k_blk, const void* v_blk,
+                                           void* out, float* lse, e2d2_dims dims, int S, void* workspace,
+                                           size_t ws_bytes, cudaStream_t stream) {
+    if (!q_blk || !k_pages || !v_pages || !P_dev || !out || (!k_blk != !v_blk)) return E2D2_ERR_INVALID_ARG;
+    e2d2_status s = check_dims(dims);
+    if (s != E2D2_OK) return s;
+    if (S <= 0) return E2D2_ERR_INVALID_ARG;
+    s = check_pages(pages, dims);
+    if (s != E2D2_OK) return s;
+    if (static_cast<long long>(dims.batch) * dims.q_heads * S > kMaxI32 / 8) return E2D2_ERR_SHAPE;
+    if (!aligned16(q_blk) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_blk) || !aligned16(v_blk) ||
+        !aligned16(out) || !aligned4(lse) || !aligned4(P_dev))
+        return E2D2_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < paged_workspace_bytes(dims, S)) return E2D2_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return E2D2_ERR_ALIGNMENT;
+    DeviceInfo* di = nullptr;
+    s = device_info(&di);
+    if (s != E2D2_OK) return s;
+    PagedAttnParams a;
+    a.pages = page_view(pages, dims, di);
+    a.q = static_cast<const __nv_bfloat16*>(q_blk);
+    a.k = static_cast<const __nv_bfloat16*>(k_pages);
+    a.v = static_cast<const __nv_bfloat16*>(v_pages);
+    a.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
+    a.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
+    a.P_dev = P_dev;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.batch = dims.batch;
+    a.q_heads = dims.q_heads;
+    a.group = dims.q_heads / dims.kv_heads;
+    a.S = S;
+    a.scale_log2 = scale_log2(dims);
+    switch (dims.head_dim) {
+        case 32: return launch_paged_attn<32>(a, stream);
+        case 64: return launch_paged_attn<64>(a, stream);
+        default: return launch_paged_attn<128>(a, stream);
+    }
+}
+
+e2d2_status e2d2_kv_cache_append_paged(void* k_pages, void* v_pages, e2d2_pages pages, const int* P_dev,
+                                       const void* k_new, const void* v_new, int S_new, float* weight, int* pos,
+                                       const int* tokens_dev, e2d2_dims dims, cudaStream_t stream) {
+    if (!k_pages || !v_pages || !P_dev || !k_new || !v_new) return E2D2_ERR_INVALID_ARG;
+    if (!weight != !pos || !weight != !tokens_dev) return E2D2_ERR_INVALID_ARG;
+    e2d2_status s = check_dims(dims);
+    if (s != E2D2_OK) return s;
+    if (S_new < 0) return E2D2_ERR_INVALID_ARG;
+    s = check_pages(pages, dims);
+    if (s != E2D2_OK) return s;
+    if (S_new > row_capacity(pages)) return E2D2_ERR_CAPACITY;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_new) || !aligned16(v_new) || !aligned4(P_dev) ||
+        !aligned4(weight) || !aligned4(pos) || !aligned4(tokens_dev))
+        return E2D2_ERR_ALIGNMENT;
+    if (S_new == 0) return E2D2_OK;
+    DeviceInfo* di = nullptr;
+    s = device_info(&di);
+    if (s != E2D2_OK) return s;
+    PagedAppendParams a;
+    a.pages = page_view(pages, dims, di);
+    a.pool[0] = static_cast<uint4*>(k_pages);
+    a.pool[1] = static_cast<uint4*>(v_pages);
+    a.src[0] = static_cast<const uint4*>(k_new);
+    a.src[1] = static_cast<const uint4*>(v_new);
+    a.P_dev = P_dev;
+    a.weight = weight;
+    a.pos = pos;
+    a.tokens = tokens_dev;
+    a.batch = dims.batch;
+    a.S_new = S_new;
+    a.vec_per_row = dims.head_dim / 8;
+    const long long total = static_cast<long long>(dims.batch) * dims.kv_heads * S_new * a.vec_per_row;
+    return launch_pdl(kv_append_paged_kernel, dim3(copy_blocks(total, di), 2), dim3(256), 0, stream, a) == cudaSuccess
+               ? E2D2_OK
+               : E2D2_ERR_CUDA;
+}
+
+e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages pages, const int* P_dev,
+                                const float* lse, const float* weight, float* weight_out, e2d2_dims dims, int S,
+                                cudaStream_t stream) {
+    if (!q || !k_pages || !P_dev || !lse || !weight || !weight_out) return E2D2_ERR_INVALID_ARG;
+    e2d2_status s = check_dims(dims);
+    if (s != E2D2_OK) return s;
+    if (S <= 0) return E2D2_ERR_INVALID_ARG;
+    s = check_pages(pages, dims);
+    if (s != E2D2_OK) return s;
+    if (static_cast<long long>(dims.batch) * dims.q_heads * S > kMaxI32 / 8) return E2D2_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned4(P_dev) || !aligned4(lse) || !aligned4(weight) ||
+        !aligned4(weight_out))
+        return E2D2_ERR_ALIGNMENT;
+    DeviceInfo* di = nullptr;
+    s = device_info(&di);
+    if (s != E2D2_OK) return s;
+    WeighParams a;
+    a.pages = page_view(pages, dims, di);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k_pages);
+    a.P_dev = P_dev;
+    a.lse = lse;
+    a.weight = weight;
+    a.weight_out = weight_out;
+    a.batch = dims.batch;
+    a.q_heads = dims.q_heads;
+    a.group = dims.q_heads / dims.kv_heads;
+    a.S = S;
+    a.scale_log2 = scale_log2(dims);
+    const int cap = static_cast<int>(row_capacity(pages));
+    switch (dims.head_dim) {
+        case 32: return launch_weigh<32>(a, cap, di, stream);
+        case 64: return launch_weigh<64>(a, cap, di, stream);
+        default: return launch_weigh<128>(a, cap, di, stream);
+    }
+}
+
+size_t e2d2_kv_cache_evict_workspace(e2d2_dims dims, e2d2_pages pages) {
+    if (check_dims(dims) != E2D2_OK || check_pages(pages, dims) != E2D2_OK) return 0;
+    return evict_workspace_bytes(dims, pages);
+}
+
+e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, const int* P_dev,
+                                const float* weight, const int* pos, const int* tokens_dev, int keep, int recent,
+                                float* weight_out, int* pos_out, int* P_out, e2d2_dims dims, void* workspace,
+                                size_t ws_bytes, cudaStream_t stream) {
+    if (!k_pages || !v_pages || !P_dev || !weight || !pos || !tokens_dev || !weight_out || !pos_out || !P_out)
+        return E2D2_ERR_INVALID_ARG;
+    e2d2_status s = check_dims(dims);
+    if (s != E2D2_OK) return s;
+    if (keep < 0 || recent < 0 || recent > keep) return E2D2_ERR_INVALID_ARG;
+    s = check_pages(pages, dims);
+    if (s != E2D2_OK) return s;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(P_dev) || !aligned4(weight) || !aligned4(pos) ||
+        !aligned4(tokens_dev) || !aligned4(weight_out) || !aligned4(pos_out) || !aligned4(P_out))
+        return E2D2_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < evict_workspace_bytes(dims, pages)) return E2D2_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return E2D2_ERR_ALIGNMENT;
+    DeviceInfo* di = nullptr;
+    s = device_info(&di);
+    if (s != E2D2_OK) return s;
+    EvictParams a;
+    a.pages = page_view(pages, dims, di);
+    a.pool[0] = static_cast<uint4*>(k_pages);
+    a.pool[1] = static_cast<uint4*>(v_pages);
+    a.P_dev = P_dev;
+    a.weight = weight;
+    a.pos = pos;
+    a.tokens = tokens_dev;
+    a.weight_out = weight_out;
+    a.pos_out = pos_out;
+    a.P_out = P_out;
+    a.ws = static_cast<int*>(workspace);
+    a.batch = dims.batch;
+    a.keep = keep;
+    a.recent = recent;
+    a.vec_per_row = dims.head_dim / 8;
+    a.list_rows = static_cast<int>(evict_list_rows(pages));
+    a.ws_stride = 4 + 2ll * a.list_rows;
+    const unsigned units = static_cast<unsigned>(dims.batch) * dims.kv_heads;
+    if (launch_pdl(kv_evict_select_kernel, dim3(units), dim3(kEvictThreads), 0, stream, a) != cudaSuccess)
+        return E2D2_ERR_CUDA;
+    const long long most = static_cast<long long>(a.list_rows) * 2 * a.vec_per_row;  // thread-steps of a unit
+    unsigned x = (di->sms * 8 + units - 1) / units;
+    if (x > (most + 255) / 256) x = static_cast<unsigned>((most + 255) / 256);
+    return launch_pdl(kv_evict_move_kernel, dim3(x, units), dim3(256), 0, stream, a) == cudaSuccess ? E2D2_OK
+                                                                                                    : E2D2_ERR_CUDA;
 }
 
 }  // extern "C"

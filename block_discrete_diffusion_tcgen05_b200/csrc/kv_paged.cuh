@@ -1,0 +1,89 @@
+// kv_paged.cuh -- what every call on a paged KV cache shares (the view of the pool through the page
+// table), and the append to it.
+//
+// A pool holds num_pages pages of page_rows rows for every kv head, [num_pages][kv_heads][page_rows][d];
+// entry b's row r is row r mod page_rows of page table[b][r / page_rows].  Without a table the pool is
+// one contiguous cache per entry: entry b is page b, and a page holds the entry's whole capacity.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "fmha_sm100.cuh"
+#include "ptx_sm100.cuh"
+
+namespace e2d2 {
+
+// Bit of the device error word: a page id outside the pool was met below an entry's length.
+constexpr unsigned int kErrBadPage = 4u;
+constexpr int kPagedMaxBatch = 1024;  // entries of a call (the prefix table of its schedule)
+
+struct PageView {
+    const int* table;  // [batch][max_pages], null: entry b is page b
+    int num_pages, page_rows, max_pages;
+    int kv_heads;
+    unsigned int* err;
+
+    __device__ __forceinline__ int capacity() const { return max_pages * page_rows; }
+
+    // Page that holds row r of entry b (r inside the capacity); -1, with the error recorded, if the
+    // table names no page of the pool.  Nothing is read or written through such an entry.
+    __device__ __forceinline__ int page_of(int b, int r) const {
+        if (table == nullptr) return b;
+        const int pg = __ldg(table + static_cast<size_t>(b) * max_pages + r / page_rows);
+        if (static_cast<unsigned>(pg) < static_cast<unsigned>(num_pages)) return pg;
+        atomicOr(err, kErrBadPage);
+        return -1;
+    }
+
+    // Row of the pool (in rows of d elements) that holds row r of entry b, head h; -1 as above.  64 bits:
+    // a pool has more elements than 32 bits count.
+    __device__ __forceinline__ long long pool_row(int b, int h, int r) const {
+        const int pg = page_of(b, r);
+        if (pg < 0) return -1;
+        const int in_page = table == nullptr ? r : r % page_rows;
+        return (static_cast<long long>(pg) * kv_heads + h) * page_rows + in_page;
+    }
+};
+
+struct PagedAppendParams {
+    PageView pages;
+    uint4* pool[2];       // K, V pools
+    const uint4* src[2];  // new rows [B][Hkv][S_new][D]
+    const int* P_dev;
+    float* weight;        // [B][Hkv][capacity] or null: the new rows' accumulated weight becomes 0,
+    int* pos;             // [B][Hkv][capacity] or null: their position tokens[b] + i
+    const int* tokens;
+    int batch, S_new, vec_per_row;
+};
+
+// A pure copy, HBM-bound: 16 bytes per thread-step, grid-stride over the rows of K (blockIdx.y == 0) and V
+// (blockIdx.y == 1); the first thread of a K row also writes its weight and position.
+__global__ void __launch_bounds__(256) kv_append_paged_kernel(const __grid_constant__ PagedAppendParams a) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();  // the previous kernel may still read the pool or write the new rows
+    const int which = blockIdx.y;
+    uint4* __restrict__ dst = a.pool[which];
+    const uint4* __restrict__ src = a.src[which];
+    const int Hkv = a.pages.kv_heads, cap = a.pages.capacity();
+    const long long total = static_cast<long long>(a.batch) * Hkv * a.S_new * a.vec_per_row;
+    for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < total;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const long long srow = i / a.vec_per_row;
+        const int vec = static_cast<int>(i - srow * a.vec_per_row);
+        const long long unit = srow / a.S_new;
+        const int s = static_cast<int>(srow - unit * a.S_new);
+        const int b = static_cast<int>(unit / Hkv), h = static_cast<int>(unit - static_cast<long long>(b) * Hkv);
+        const long long r = static_cast<long long>(ragged_clamp(__ldg(a.P_dev + b), cap)) + s;
+        if (r >= cap) continue;  // rows past the capacity are not written
+        if (which == 0 && vec == 0 && a.weight != nullptr) {
+            const long long w = unit * cap + r;
+            a.weight[w] = 0.f;
+            a.pos[w] = __ldg(a.tokens + b) + s;
+        }
+        const long long d = a.pages.pool_row(b, h, static_cast<int>(r));
+        if (d >= 0) dst[d * a.vec_per_row + vec] = __ldg(src + i);
+    }
+}
+
+}  // namespace e2d2

@@ -59,7 +59,8 @@ typedef enum {
     E2D2_ERR_WORKSPACE = 6,   /* workspace missing or smaller than the _workspace query     */
     E2D2_ERR_CUDA = 7,        /* a CUDA runtime / driver call failed                        */
     E2D2_ERR_TIMEOUT = 8,     /* a bounded device-side wait gave up (see e2d2_last_device_error) */
-    E2D2_ERR_DEVICE_CHECK = 9 /* debug library: a device-side bounds check failed              */
+    E2D2_ERR_DEVICE_CHECK = 9, /* debug library: a device-side bounds check failed             */
+    E2D2_ERR_PAGE = 10        /* a page table named a page outside the pool (see e2d2_last_device_error) */
 } e2d2_status;
 
 typedef struct {
@@ -314,6 +315,97 @@ E2D2_API e2d2_status e2d2_kv_cache_append_ragged(void* k_cache, void* v_cache, i
                                                  const void* k_new, const void* v_new, int S_new, e2d2_dims dims,
                                                  cudaStream_t stream);
 
+/*
+ * Paged KV cache.  A pool holds num_pages pages, each page_rows rows of every kv head:
+ * k_pages, v_pages [num_pages][kv_heads][page_rows][d].  Row r of batch entry b is row
+ * r mod page_rows of page page_table[b][r / page_rows]; an entry holds up to
+ * max_pages * page_rows rows (its row capacity).
+ *   page_table: DEVICE array [batch][max_pages] of ints (4-byte aligned), read by the kernels; only
+ *   the pages of rows that a call reads or writes are looked up, the others may hold anything.
+ *   page_rows: a multiple of 16 (else E2D2_ERR_UNSUPPORTED).
+ *   page_table == NULL: contiguous caches [batch][kv_heads][capacity][d] -- the layout of the other
+ *   calls -- as one page per entry: num_pages = batch, max_pages = 1, page_rows = capacity (any).
+ *   A looked-up page id outside [0, num_pages) is never followed: its rows are not written and take
+ *   no part in attention, and e2d2_last_device_error() reports E2D2_ERR_PAGE.
+ *   Entries may share pages (a common prefix) as long as no call writes to a shared page.
+ *   batch <= 1024, batch * kv_heads <= 65535, row capacity < 2^30 (else E2D2_ERR_SHAPE).
+ * P_dev: DEVICE array of batch ints, the rows each entry holds, read by the kernels and clamped to
+ * [0, row capacity].
+ */
+typedef struct {
+    int num_pages;
+    int page_rows;
+    int max_pages;
+    const int* page_table;
+} e2d2_pages;
+
+/*
+ * Sampling step over a paged cache: as e2d2_attn_decoder_sample_ragged, with the cached rows found
+ * through the page table.  S = 1 is the step of one new token (a block of one token: autoregressive
+ * decoding).  k_blk and v_blk may both be NULL: the queries then see the cached rows only (for a
+ * caller that has appended the block already), and a row that sees nothing (P = 0) gets a zero
+ * output and lse = -infinity.
+ *   workspace: at least e2d2_attn_decoder_sample_paged_workspace(dims, S) bytes (0 for invalid
+ *   arguments; needs no GPU), 16-byte aligned, zero-filled once; completed calls leave it reusable
+ *   on the same stream.  Calls that may run at the same time need different workspaces.  After
+ *   E2D2_ERR_TIMEOUT it must be zero-filled again.
+ */
+E2D2_API size_t e2d2_attn_decoder_sample_paged_workspace(e2d2_dims dims, int S);
+
+E2D2_API e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_pages, const void* v_pages,
+                                                    e2d2_pages pages, const int* P_dev, const void* k_blk,
+                                                    const void* v_blk, void* out, float* lse, e2d2_dims dims, int S,
+                                                    void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Append to a paged cache: as e2d2_kv_cache_append_ragged, rows P_dev[b]..P_dev[b]+S_new-1 of entry
+ * b found through the page table; rows at or past the row capacity are not written, S_new above it
+ * is E2D2_ERR_CAPACITY.  The pages that are written must be the entry's own.
+ *   weight [batch][kv_heads][row capacity] float, pos the same shape int, tokens_dev DEVICE
+ *   [batch] ints: all three or none.  With them the new rows' accumulated weight becomes 0 and
+ *   their position tokens_dev[b] + i (tokens_dev[b]: tokens the entry has seen before the block),
+ *   as e2d2_kv_cache_evict wants them.
+ */
+E2D2_API e2d2_status e2d2_kv_cache_append_paged(void* k_pages, void* v_pages, e2d2_pages pages, const int* P_dev,
+                                                const void* k_new, const void* v_new, int S_new, float* weight,
+                                                int* pos, const int* tokens_dev, e2d2_dims dims,
+                                                cudaStream_t stream);
+
+/*
+ * Accumulated attention weight of the cached rows: for j < P_dev[b]
+ *   weight_out[b][h][j] = weight[b][h][j] + sum_i exp(scale q_i.k_j - lse_i)
+ * over the G * S query rows i that read kv head h; rows at or past P_dev[b] are not written.
+ *   q [batch][q_heads][S][d] and lse [batch][q_heads][S]: the queries and the log-sum-exp of an
+ *   attention call (which may have seen more rows than these); a row with lse = -infinity adds
+ *   nothing.  weight_out is weight itself (in place) or does not overlap it.  No atomics: two calls
+ *   with the same inputs give the same bits.
+ */
+E2D2_API e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages pages, const int* P_dev,
+                                         const float* lse, const float* weight, float* weight_out, e2d2_dims dims,
+                                         int S, cudaStream_t stream);
+
+/*
+ * Eviction by accumulated weight: every (entry, kv head) of more than `keep` rows keeps `keep` of
+ * its P_dev[b] rows -- those at positions >= tokens_dev[b] - recent first (pos; the newest
+ * `recent` tokens, 0 <= recent <= keep), then by decreasing weight, ties to the lowest row; a NaN
+ * weight counts as below every number, -0 as 0.  Kept rows below `keep` stay where they are, and
+ * the i-th kept row at or past `keep` moves, K, V, weight and position, to the i-th row below
+ * `keep` that is not kept.  Attention does not depend on the order of the cached rows; pos keeps
+ * each row's token.  Entries of at most `keep` rows stay as they are.
+ *   weight_out, pos_out: rows below min(P, keep) written, the others not; each is its input (in
+ *   place) or does not overlap it.  P_out [batch]: min(P, keep); may be P_dev.  Cache rows at or
+ *   past P_out[b] keep their bits and need not be kept.
+ *   Every page of rows below P must be the entry's own (not shared).
+ *   workspace: at least e2d2_kv_cache_evict_workspace(dims, pages) bytes, 16-byte aligned, contents
+ *   ignored; calls that may run at the same time need different workspaces.
+ */
+E2D2_API size_t e2d2_kv_cache_evict_workspace(e2d2_dims dims, e2d2_pages pages);
+
+E2D2_API e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, const int* P_dev,
+                                         const float* weight, const int* pos, const int* tokens_dev, int keep,
+                                         int recent, float* weight_out, int* pos_out, int* P_out, e2d2_dims dims,
+                                         void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 E2D2_API const char* e2d2_status_string(e2d2_status status);
 
@@ -323,7 +415,8 @@ E2D2_API const char* e2d2_status_string(e2d2_status status);
  * Python binding when the environment variable E2D2_DEBUG=1), a device-side bounds check on a
  * TMA coordinate or a work-unit index failed; else E2D2_ERR_TIMEOUT if a bounded device-side wait
  * gave up since the last read.  After either, outputs of the affected calls are undefined and
- * sampling workspaces must be zero-filled again.
+ * sampling workspaces must be zero-filled again.  E2D2_ERR_PAGE if neither happened but a page table
+ * named a page outside the pool.
  */
 E2D2_API e2d2_status e2d2_last_device_error(cudaStream_t stream);
 
