@@ -22,6 +22,7 @@
 #include "kv_append.cuh"
 #include "kv_evict.cuh"
 #include "kv_paged.cuh"
+#include "kv_weigh.cuh"
 #include "paged_attn.cuh"
 
 namespace e2d2 {
@@ -968,12 +969,29 @@ unsigned copy_blocks(long long items, const DeviceInfo* di) {
     return static_cast<unsigned>(blocks < 1 ? 1 : blocks);
 }
 
+template <int D, int MT, int RW>
+e2d2_status launch_paged(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
+    using C = PagedCfg<D, MT, RW>;
+    auto kern = paged_attn_kernel<D, MT, RW>;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC) != cudaSuccess)
+            return E2D2_ERR_CUDA;
+        configured_dev = dev;
+    }
+    const int grid = 2 * di->sms < kPagedMaxCtas ? 2 * di->sms : kPagedMaxCtas;
+    return launch_pdl(kern, dim3(grid), dim3(kPagedThreads), C::ALLOC, stream, a) == cudaSuccess ? E2D2_OK
+                                                                                                 : E2D2_ERR_CUDA;
+}
+
 template <int D>
-e2d2_status launch_paged_attn(const PagedAttnParams& a, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(a.batch) * a.q_heads * a.S;
-    return launch_pdl(paged_attn_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, a) == cudaSuccess
-               ? E2D2_OK
-               : E2D2_ERR_CUDA;
+e2d2_status launch_paged_rows(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
+    if (a.rows <= 16) return launch_paged<D, 1, 1>(a, di, stream);
+    if (a.rows <= 32) return launch_paged<D, 2, 1>(a, di, stream);
+    if (a.rows <= 64) return launch_paged<D, 2, 2>(a, di, stream);
+    return launch_paged<D, 2, 4>(a, di, stream);
 }
 
 template <int D>
@@ -986,11 +1004,21 @@ e2d2_status launch_weigh(const WeighParams& a, int capacity, const DeviceInfo* d
                                                                                                   : E2D2_ERR_CUDA;
 }
 
-size_t paged_workspace_bytes(const e2d2_dims& dims, int S) {
-    (void)dims;
-    (void)S;
-    return 1024;
+struct PagedLayout {
+    int rows_cap, slot_floats;
+    size_t bytes;
+};
+
+// Tickets, then two partial slots per block: rows of D floats, their maxima and sums.
+PagedLayout paged_layout(const e2d2_dims& dims, int S) {
+    PagedLayout w;
+    const long long rows = static_cast<long long>(dims.q_heads / dims.kv_heads) * S;
+    w.rows_cap = static_cast<int>(rows < 128 ? rows : 128);
+    w.slot_floats = (w.rows_cap * (dims.head_dim + 2) + 31) / 32 * 32;
+    w.bytes = 2048 + static_cast<size_t>(2) * kPagedMaxCtas * w.slot_floats * sizeof(float);
+    return w;
 }
+static_assert(kPagedMaxCtas * sizeof(int) <= 2048, "tickets");
 
 // Rows that one list of an eviction can hold, rounded to whole 16 bytes.
 long long evict_list_rows(const e2d2_pages& pg) { return (row_capacity(pg) / 2 + 4) / 4 * 4; }
@@ -1005,7 +1033,7 @@ extern "C" {
 
 size_t e2d2_attn_decoder_sample_paged_workspace(e2d2_dims dims, int S) {
     if (check_dims(dims) != E2D2_OK || S <= 0) return 0;
-    return paged_workspace_bytes(dims, S);
+    return paged_layout(dims, S).bytes;
 }
 
 e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_pages, const void* v_pages,
@@ -1022,30 +1050,44 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     if (!aligned16(q_blk) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_blk) || !aligned16(v_blk) ||
         !aligned16(out) || !aligned4(lse) || !aligned4(P_dev))
         return E2D2_ERR_ALIGNMENT;
-    if (!workspace || ws_bytes < paged_workspace_bytes(dims, S)) return E2D2_ERR_WORKSPACE;
+    const PagedLayout w = paged_layout(dims, S);
+    if (!workspace || ws_bytes < w.bytes) return E2D2_ERR_WORKSPACE;
     if (!aligned16(workspace)) return E2D2_ERR_ALIGNMENT;
     DeviceInfo* di = nullptr;
     s = device_info(&di);
     if (s != E2D2_OK) return s;
+    const int D = dims.head_dim;
+    const long long BHkv = static_cast<long long>(dims.batch) * dims.kv_heads;
     PagedAttnParams a;
+    const long long units = static_cast<long long>(pages.num_pages) * dims.kv_heads;
+    bool ok = map_3d(&a.tm_k, k_pages, D, pages.page_rows, units, pages.page_rows, 16) &&
+              map_3d(&a.tm_v, v_pages, D, pages.page_rows, units, pages.page_rows, 16);
+    if (ok && k_blk)
+        ok = map_3d(&a.tm_k1, k_blk, D, S, BHkv, S, 16) && map_3d(&a.tm_v1, v_blk, D, S, BHkv, S, 16);
+    if (!ok) return E2D2_ERR_CUDA;
+    if (!k_blk) a.tm_k1 = a.tm_k, a.tm_v1 = a.tm_v;
     a.pages = page_view(pages, dims, di);
-    a.q = static_cast<const __nv_bfloat16*>(q_blk);
-    a.k = static_cast<const __nv_bfloat16*>(k_pages);
-    a.v = static_cast<const __nv_bfloat16*>(v_pages);
-    a.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
-    a.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
+    a.q = static_cast<const uint4*>(q_blk);
     a.P_dev = P_dev;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
+    a.tickets = static_cast<int*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2048);
+    a.err = di->err;
     a.batch = dims.batch;
     a.q_heads = dims.q_heads;
     a.group = dims.q_heads / dims.kv_heads;
     a.S = S;
+    a.own = k_blk != nullptr;
+    a.rows = a.group * S;
+    a.qtiles = (a.rows + 127) / 128;
+    a.rows_cap = w.rows_cap;
+    a.slot_floats = w.slot_floats;
     a.scale_log2 = scale_log2(dims);
-    switch (dims.head_dim) {
-        case 32: return launch_paged_attn<32>(a, stream);
-        case 64: return launch_paged_attn<64>(a, stream);
-        default: return launch_paged_attn<128>(a, stream);
+    switch (D) {
+        case 32: return launch_paged_rows<32>(a, di, stream);
+        case 64: return launch_paged_rows<64>(a, di, stream);
+        default: return launch_paged_rows<128>(a, di, stream);
     }
 }
 
