@@ -994,14 +994,28 @@ e2d2_status launch_paged_rows(const PagedAttnParams& a, const DeviceInfo* di, cu
     return launch_paged<D, 2, 4>(a, di, stream);
 }
 
+template <int D, int N>
+e2d2_status launch_weigh(const WeighParams& a, const DeviceInfo* di, cudaStream_t stream) {
+    using C = WeighCfg<D, N>;
+    auto kern = kv_weigh_kernel<D, N>;
+    // at least ~116 KB, so that no two blocks share an SM: at N = 256 each takes all of its tensor memory
+    const int smem = C::ALLOC > 118784 ? C::ALLOC : 118784;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return E2D2_ERR_CUDA;
+        configured_dev = dev;
+    }
+    return launch_pdl(kern, dim3(di->sms), dim3(kWeighThreads), smem, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
+}
+
 template <int D>
-e2d2_status launch_weigh(const WeighParams& a, int capacity, const DeviceInfo* di, cudaStream_t stream) {
-    const unsigned units = static_cast<unsigned>(a.batch) * a.pages.kv_heads;
-    unsigned x = (di->sms * 8 + units - 1) / units;
-    const unsigned most = static_cast<unsigned>((capacity + 7) / 8);
-    if (x > most) x = most;
-    return launch_pdl(kv_weigh_kernel<D>, dim3(x, units), dim3(256), 0, stream, a) == cudaSuccess ? E2D2_OK
-                                                                                                  : E2D2_ERR_CUDA;
+e2d2_status launch_weigh_rows(const WeighParams& a, const DeviceInfo* di, cudaStream_t stream) {
+    if (a.n <= 32) return launch_weigh<D, 32>(a, di, stream);
+    if (a.n <= 64) return launch_weigh<D, 64>(a, di, stream);
+    return launch_weigh<D, 256>(a, di, stream);
 }
 
 struct PagedLayout {
@@ -1144,25 +1158,39 @@ e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages p
     DeviceInfo* di = nullptr;
     s = device_info(&di);
     if (s != E2D2_OK) return s;
+    const int D = dims.head_dim;
+    const int rows = dims.q_heads / dims.kv_heads * S;
+    // boxes of the largest power of two rows, 128 at most, that divides a page
+    int box = 128;
+    if (pages.page_table)
+        while (pages.page_rows % box != 0) box /= 2;
     WeighParams a;
+    if (!map_3d(&a.tm_k, k_pages, D, pages.page_rows, static_cast<long long>(pages.num_pages) * dims.kv_heads,
+                pages.page_rows, box) ||
+        !map_2d(&a.tm_q, q, D, static_cast<long long>(dims.batch) * dims.q_heads * S, 16))
+        return E2D2_ERR_CUDA;
     a.pages = page_view(pages, dims, di);
-    a.q = static_cast<const __nv_bfloat16*>(q);
-    a.k = static_cast<const __nv_bfloat16*>(k_pages);
     a.P_dev = P_dev;
     a.lse = lse;
-    a.weight = weight;
     a.weight_out = weight_out;
+    a.err = di->err;
     a.batch = dims.batch;
-    a.q_heads = dims.q_heads;
-    a.group = dims.q_heads / dims.kv_heads;
-    a.S = S;
+    a.box_rows = box;
+    a.rows = rows;
     a.scale_log2 = scale_log2(dims);
-    const int cap = static_cast<int>(row_capacity(pages));
-    switch (dims.head_dim) {
-        case 32: return launch_weigh<32>(a, cap, di, stream);
-        case 64: return launch_weigh<64>(a, cap, di, stream);
-        default: return launch_weigh<128>(a, cap, di, stream);
+    // one launch for every 256 query rows of a head, each adding to the last one's sums
+    for (int r = 0; r < rows; r += kWeighMaxRows) {
+        a.row0 = r;
+        a.n = rows - r < kWeighMaxRows ? rows - r : kWeighMaxRows;
+        a.weight = r == 0 ? weight : weight_out;
+        switch (D) {
+            case 32: s = launch_weigh_rows<32>(a, di, stream); break;
+            case 64: s = launch_weigh_rows<64>(a, di, stream); break;
+            default: s = launch_weigh_rows<128>(a, di, stream); break;
+        }
+        if (s != E2D2_OK) return s;
     }
+    return E2D2_OK;
 }
 
 size_t e2d2_kv_cache_evict_workspace(e2d2_dims dims, e2d2_pages pages) {

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const __
     ptx::griddep_wait();
     const int unit = blockIdx.x, Hkv = p.pages.kv_heads, cap = p.pages.capacity();
     const int b = unit / Hkv, tid = threadIdx.x;
-    const int P = ragged_clamp(__ldg(p.P_dev + b), cap);
+    const int P = ragged_clamp(__ldcg(p.P_dev + b), cap);
     const float* w = p.weight + static_cast<long long>(unit) * cap;
     const int* pos = p.pos + static_cast<long long>(unit) * cap;
     float* w_out = p.weight_out + static_cast<long long>(unit) * cap;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const __
         return;
     }
     // the first protected position, without overflow for any recent >= 0
-    const long long pf = static_cast<long long>(__ldg(p.tokens + b)) - p.recent;
+    const long long pf = static_cast<long long>(__ldcg(p.tokens + b)) - p.recent;
     const int protect = pf < INT_MIN ? INT_MIN : static_cast<int>(pf);
     // Radix selection of the keep-th largest rank, eight bits a pass: prefix = its leading bits, need = how
     // many rows with that prefix stay.

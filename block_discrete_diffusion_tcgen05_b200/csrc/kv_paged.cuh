@@ -18,6 +18,8 @@ namespace e2d2 {
 constexpr unsigned int kErrBadPage = 4u;
 constexpr int kPagedMaxBatch = 1024;  // entries of a call (the prefix table of its schedule)
 
+// What a call reads (lengths, tables, queries, weights) may come from the kernel ahead of it on the stream,
+// which it overlaps until griddepcontrol.wait: such values are read through L2 (ld.cg), never as read-only.
 struct PageView {
     const int* table;  // [batch][max_pages], null: entry b is page b
     int num_pages, page_rows, max_pages;
@@ -30,7 +32,7 @@ struct PageView {
     // table names no page of the pool.  Nothing is read or written through such an entry.
     __device__ __forceinline__ int page_of(int b, int r) const {
         if (table == nullptr) return b;
-        const int pg = __ldg(table + static_cast<size_t>(b) * max_pages + r / page_rows);
+        const int pg = __ldcg(table + static_cast<size_t>(b) * max_pages + r / page_rows);
         if (static_cast<unsigned>(pg) < static_cast<unsigned>(num_pages)) return pg;
         atomicOr(err, kErrBadPage);
         return -1;
@@ -45,6 +47,47 @@ struct PageView {
         return (static_cast<long long>(pg) * kv_heads + h) * page_rows + in_page;
     }
 };
+
+// The work of a call as one stream: entry b takes count(b) items.  Fills pre[0..batch-1] with the items before
+// each entry (shared memory, as is sums[THREADS / 32]) and returns the sum of all.  Every thread of a block of
+// THREADS calls it; pre is readable after it.
+template <int THREADS, class Count>
+__device__ __forceinline__ long long stream_prefix(int batch, long long* pre, long long* sums, Count count) {
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int per = (batch + THREADS - 1) / THREADS, b0 = tid * per;
+    long long mine = 0;
+    for (int i = b0; i < b0 + per && i < batch; ++i) mine += count(i);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        before += w < warp ? sums[w] : 0;
+        total += sums[w];
+    }
+    for (int i = b0; i < b0 + per && i < batch; ++i) {
+        pre[i] = before;
+        before += count(i);
+    }
+    __syncthreads();
+    return total;
+}
+
+// The entry that holds item pos of the stream: pre[b] <= pos.
+__device__ __forceinline__ int stream_entry(const long long* pre, int batch, long long pos) {
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= pos) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
 
 struct PagedAppendParams {
     PageView pages;
@@ -74,15 +117,15 @@ __global__ void __launch_bounds__(256) kv_append_paged_kernel(const __grid_const
         const long long unit = srow / a.S_new;
         const int s = static_cast<int>(srow - unit * a.S_new);
         const int b = static_cast<int>(unit / Hkv), h = static_cast<int>(unit - static_cast<long long>(b) * Hkv);
-        const long long r = static_cast<long long>(ragged_clamp(__ldg(a.P_dev + b), cap)) + s;
+        const long long r = static_cast<long long>(ragged_clamp(__ldcg(a.P_dev + b), cap)) + s;
         if (r >= cap) continue;  // rows past the capacity are not written
         if (which == 0 && vec == 0 && a.weight != nullptr) {
             const long long w = unit * cap + r;
             a.weight[w] = 0.f;
-            a.pos[w] = __ldg(a.tokens + b) + s;
+            a.pos[w] = __ldcg(a.tokens + b) + s;
         }
         const long long d = a.pages.pool_row(b, h, static_cast<int>(r));
-        if (d >= 0) dst[d * a.vec_per_row + vec] = __ldg(src + i);
+        if (d >= 0) dst[d * a.vec_per_row + vec] = __ldcg(src + i);
     }
 }
 

@@ -1,57 +1,314 @@
 // kv_weigh.cuh -- accumulated attention weight of a cache's rows: with the lse of an attention call,
 //
 //   weight_out_j = weight_j + sum_i exp(scale q_i . k_j - lse_i)      (i over the G S rows that read kv head h)
+//
+// K is read once and nothing else is large, so the kernel is bound by HBM for up to some 160 query rows (then by
+// the exponentials: 16 a clock and SM against 22 bytes of K).  The scores are taken transposed, S^T = K Q^T with
+// 128 keys on the tensor-memory lanes: a thread of the epilogue holds one key's scores, so the sum over the
+// query rows is a sum in its own registers -- no shuffles, no atomics, one order -- and the normaliser is known
+// (lse), so there is no maximum to track.
+//
+// Warp 0 loads (a ring of key tiles of 128 rows, in boxes that end where pages do; Q once per unit), warp 1
+// issues the products into two buffers of tensor memory, and two warpgroups take the tiles in turn: one reads
+// its scores while the other's are computed.  The tiles of all (entry, kv head) units form one stream cut
+// evenly over a persistent grid.
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "kv_paged.cuh"
 
 namespace e2d2 {
 
-struct WeighParams {
+constexpr int kWeighThreads = 384;  // 12 warps: loads, products, two idle, two epilogue warpgroups
+constexpr int kWeighKeys = 128;
+constexpr int kWeighMaxRows = 256;  // query rows of one launch (columns of one product)
+
+struct alignas(64) WeighParams {
+    CUtensorMap tm_k;     // pool: 3D {D, page_rows, num_pages * Hkv}, boxes of box_rows
+    CUtensorMap tm_q;     // 2D {D, B * Hq * S}, boxes of 16 rows
     PageView pages;
-    const __nv_bfloat16* q;  // [B][Hq][S][D]
-    const __nv_bfloat16* k;
     const int* P_dev;
-    const float* lse;        // [B][Hq][S]
-    const float* weight;     // [B][Hkv][capacity]
+    const float* lse;     // [B][Hq][S]
+    const float* weight;  // [B][Hkv][capacity]
     float* weight_out;
-    int batch, q_heads, group, S;
+    unsigned int* err;
+    int batch, box_rows;
+    int rows, row0, n;    // query rows per kv head (G * S); this launch takes rows row0.., n of them
     float scale_log2;
 };
 
-// A warp per cached row (grid-stride over the rows of one (entry, kv head), blockIdx.y).
-template <int D>
-__global__ void __launch_bounds__(256) kv_weigh_kernel(const __grid_constant__ WeighParams p) {
-    constexpr int E = D / 32;
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int lane = threadIdx.x % 32;
-    const int unit = blockIdx.y, Hkv = p.pages.kv_heads, cap = p.pages.capacity();
-    const int b = unit / Hkv, h = unit % Hkv;
-    const int P = ragged_clamp(__ldg(p.P_dev + b), cap);
-    const int rows = p.group * p.S;
-    const long long row0 = (static_cast<long long>(b) * p.q_heads + h * p.group) * p.S;
-    for (int j = blockIdx.x * 8 + threadIdx.x / 32; j < P; j += gridDim.x * 8) {
-        const long long r = p.pages.pool_row(b, h, j);
-        float add = 0.f;
-        if (r >= 0) {
-            float k[E];
-            for (int e = 0; e < E; ++e) k[e] = __bfloat162float(p.k[r * D + lane * E + e]);
-            for (int i = 0; i < rows; ++i) {
-                float x = 0.f;
-                for (int e = 0; e < E; ++e) x += k[e] * __bfloat162float(p.q[(row0 + i) * D + lane * E + e]);
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                const float lse = p.lse[row0 + i];
-                add += lse == -INFINITY ? 0.f : ptx::ex2(x * p.scale_log2 - lse * 1.4426950408889634f);
+// N: columns that shared and tensor memory are laid out for (the launch's rows rounded up).
+template <int D_, int N_>
+struct WeighCfg {
+    static constexpr int D = D_, N = N_;
+    static constexpr int RB = D * 2 < 128 ? D * 2 : 128;  // bytes per row of one column chunk
+    static constexpr int NCH = D * 2 / RB;
+    static constexpr uint32_t SWZ = RB == 128 ? 2u : 4u;
+    static constexpr int QCHUNK = N * RB, Q_BYTES = NCH * QCHUNK;
+    static constexpr int KCHUNK = kWeighKeys * RB, K_BYTES = NCH * KCHUNK;
+    static constexpr int QB = N <= 64 ? 2 : 1;
+    static constexpr int FIT = (216 * 1024 - QB * Q_BYTES) / K_BYTES;
+    static constexpr int NST = FIT < 8 ? FIT : 8;
+    static constexpr uint32_t TMEM_COLS = 2 * N < 32 ? 32u : 2u * N;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + QB * Q_BYTES;
+    static constexpr int OFF_BAR = OFF_K + NST * K_BYTES;
+    // k_full[NST], k_empty[NST], q_full[QB], q_empty[QB], s_full[2], s_free[2], drain, done
+    static constexpr int NBAR = 2 * NST + 2 * QB + 6;
+    static constexpr int OFF_LSE = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // float [8 warps][N]
+    static constexpr int OFF_PRE = OFF_LSE + 8 * N * 4;                  // long long [kPagedMaxBatch]
+    static constexpr int OFF_MISC = OFF_PRE + kPagedMaxBatch * 8;        // holder, abort, scan sums
+    static constexpr int BYTES = OFF_MISC + 16 + 8 * (kWeighThreads / 32);
+    static constexpr int ALLOC = (BYTES + 1023) / 1024 * 1024 + 1024;
+    static_assert(NST >= 2 && ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
+};
+
+// Walks the tiles of this block: unit (entry b, kv head), key tile t of it.
+struct WeighWalk {
+    const WeighParams& p;
+    long long left;  // tiles still to come
+    int b, h, P, tiles;
+    int unit, t;     // the current tile's unit (b * Hkv + h) and index
+
+    __device__ WeighWalk(const WeighParams& prm, const long long* pre, long long first, long long last)
+        : p(prm), left(last - first), b(0), h(0), P(0), tiles(0), unit(0), t(0) {
+        if (left <= 0) return;
+        b = stream_entry(pre, p.batch, first);  // holds a tile, so it has rows
+        load();
+        const long long in = first - pre[b];
+        h = static_cast<int>(in / tiles);
+        t = static_cast<int>(in - static_cast<long long>(h) * tiles) - 1;
+    }
+    __device__ void load() {
+        P = ragged_clamp(__ldcg(p.P_dev + b), p.pages.capacity());
+        tiles = (P + kWeighKeys - 1) / kWeighKeys;
+    }
+    // Moves to the next tile; false at the end.
+    __device__ bool next() {
+        if (left <= 0) return false;
+        --left;
+        if (++t == tiles) {
+            t = 0;
+            if (++h == p.pages.kv_heads) {
+                h = 0;
+                do {
+                    ++b;
+                    load();
+                } while (tiles == 0);  // a tile is left, so an entry with rows follows
             }
         }
+        unit = b * p.pages.kv_heads + h;
+        return true;
+    }
+};
+
+template <int D, int N>
+__global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid_constant__ WeighParams p) {
+    using C = WeighCfg<D, N>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_empty = k_full + C::NST;
+    uint64_t* q_full = k_empty + C::NST;
+    uint64_t* q_empty = q_full + C::QB;
+    uint64_t* s_full = q_empty + C::QB;
+    uint64_t* s_free = s_full + 2;
+    uint64_t* drain = s_free + 2;
+    uint64_t* done = drain + 1;
+    long long* pre = reinterpret_cast<long long*>(smem + C::OFF_PRE);
+    uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    long long* sums = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);
+
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NST; ++i) ptx::mbar_init(&k_full[i], 1), ptx::mbar_init(&k_empty[i], 1);
+        for (int i = 0; i < C::QB; ++i) ptx::mbar_init(&q_full[i], 1), ptx::mbar_init(&q_empty[i], 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 128);
+        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(done, 256);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(holder, C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
+    const int cap = p.pages.capacity(), Hkv = p.pages.kv_heads;
+    const long long total = stream_prefix<kWeighThreads>(p.batch, pre, sums, [&](int i) {
+        return static_cast<long long>(Hkv) * ((ragged_clamp(__ldcg(p.P_dev + i), cap) + kWeighKeys - 1) / kWeighKeys);
+    });
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *holder;
+    const long long first = range_begin(blockIdx.x, total, gridDim.x), last = range_begin(blockIdx.x + 1, total, gridDim.x);
+    const int n16 = round16(p.n);
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loads
+        // Lane j looks up and loads box j of a tile; the next tile's look-up is done while this one waits.
         if (lane == 0) {
-            const long long w = static_cast<long long>(unit) * cap + j;
-            p.weight_out[w] = p.weight[w] + add;
+            ptx::tma_prefetch_desc(&p.tm_k);
+            ptx::tma_prefetch_desc(&p.tm_q);
         }
+        test_producer_delay();
+        const int boxes = kWeighKeys / p.box_rows;
+        WeighWalk walk(p, pre, first, last);
+        int unit = 0, y = -1, z = 0;
+        auto look_up = [&]() {
+            if (!walk.next()) return false;
+            unit = walk.unit;
+            const int r = walk.t * kWeighKeys + lane * p.box_rows;
+            y = -1;
+            if (lane < boxes && r < walk.P) {
+                const int pg = p.pages.page_of(walk.b, r);
+                y = p.pages.table == nullptr ? r : r % p.pages.page_rows;
+                z = pg < 0 ? p.pages.num_pages * Hkv : (p.pages.table == nullptr ? unit : pg * Hkv + unit % Hkv);
+            }
+            return true;
+        };
+        uint32_t it = 0, units = 0;
+        int have = -1;
+        bool ok = true, more = look_up();
+        while (more && ok) {
+            const int cu = unit, cy = y, cz = z;
+            more = look_up();
+            if (cu != have) {
+                const uint32_t qb = units % C::QB;
+                ok = wait_bar_warp(&q_empty[qb], ((units / C::QB) & 1) ^ 1, abort_flag, p.err);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&q_full[qb], n16 * D * 2);
+                    const int row = cu * p.rows + p.row0;  // packed rows of a unit are contiguous
+                    for (int ch = 0; ch < C::NCH; ++ch)
+                        for (int r = 0; r < n16; r += 16)
+                            ptx::tma_load_2d(&p.tm_q, &q_full[qb], smem + C::OFF_Q + qb * C::Q_BYTES + ch * C::QCHUNK + r * C::RB,
+                                             ch * 64, row + r);
+                }
+                __syncwarp();
+                ++units;
+                have = cu;
+            }
+            const uint32_t st = it % C::NST;
+            ok = wait_bar_warp(&k_empty[st], ((it / C::NST) & 1) ^ 1, abort_flag, p.err);
+            if (!ok) break;
+            const int n = __popc(__ballot_sync(0xffffffffu, cy >= 0));
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&k_full[st], static_cast<uint32_t>(n) * p.box_rows * D * 2);
+            __syncwarp();
+            if (cy >= 0)
+                for (int ch = 0; ch < C::NCH; ++ch)
+                    ptx::tma_load_3d(&p.tm_k, &k_full[st],
+                                     smem + C::OFF_K + st * C::K_BYTES + ch * C::KCHUNK + lane * p.box_rows * C::RB, ch * 64, cy, cz);
+            __syncwarp();
+            ++it;
+        }
+        // never leave with copies in flight
+        volatile int no_abort = 0;
+        for (uint32_t i = it > C::NST ? it - C::NST : 0u; i < it; ++i)
+            wait_bar_warp(&k_full[i % C::NST], (i / C::NST) & 1, &no_abort, p.err, true);
+        for (uint32_t i = units > C::QB ? units - C::QB : 0u; i < units; ++i)
+            wait_bar_warp(&q_full[i % C::QB], (i / C::QB) & 1, &no_abort, p.err, true);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- S^T = K Q^T
+        const bool leader = ptx::elect_one();
+        const uint32_t sQ = ptx::smem_u32(smem + C::OFF_Q), sK = ptx::smem_u32(smem + C::OFF_K);
+        const uint64_t desc = ptx::smem_desc(0, 16, 8 * C::RB, C::SWZ);  // K (A) and Q (B): K-major
+        const uint32_t idesc = ptx::idesc_bf16_f32(kWeighKeys, n16, false, false);
+        constexpr int KPC = C::RB / 32;  // 16-element steps per column chunk
+        WeighWalk walk(p, pre, first, last);
+        uint32_t it = 0, units = 0;
+        int have = -1;
+        bool ok = true;
+        while (ok && walk.next()) {
+            if (walk.unit != have) {
+                if (have >= 0 && leader) ptx::mma_commit(&q_empty[(units - 1) % C::QB]);
+                __syncwarp();
+                ok = wait_bar_warp(&q_full[units % C::QB], (units / C::QB) & 1, abort_flag, p.err);
+                ++units;
+                have = walk.unit;
+            }
+            const uint32_t st = it % C::NST, sb = it & 1;
+            ok = ok && wait_bar_warp(&s_free[sb], ((it >> 1) & 1) ^ 1, abort_flag, p.err) &&
+                 wait_bar_warp(&k_full[st], (it / C::NST) & 1, abort_flag, p.err);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (leader) {
+                const uint32_t q = sQ + ((units - 1) % C::QB) * C::Q_BYTES, k = sK + st * C::K_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    ptx::mma_ss(tmem + sb * N, desc | ((k + (ks / KPC) * C::KCHUNK + (ks % KPC) * 32) >> 4),
+                                desc | ((q + (ks / KPC) * C::QCHUNK + (ks % KPC) * 32) >> 4), idesc, ks > 0 ? 1u : 0u);
+                ptx::mma_commit(&k_empty[st]);
+                ptx::mma_commit(&s_full[sb]);
+            }
+            __syncwarp();
+            ++it;
+        }
+        // tensor memory is released when this warp's products and every epilogue thread are done
+        if (leader) ptx::mma_commit(drain);
+        __syncwarp();
+        volatile int no_abort = 0;
+        wait_bar_warp(drain, 0, &no_abort, p.err, true);
+        wait_bar_warp(done, 0, &no_abort, p.err, true);
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- thread = key: sums over the columns
+        // Warpgroup g takes every other tile; every warp has its own copy of the normalisers.
+        const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane;
+        float* lse2 = reinterpret_cast<float*>(smem + C::OFF_LSE) + (warp - 4) * N;
+        WeighWalk walk(p, pre, first, last);
+        uint32_t it = 0;
+        int have = -1;
+        while (walk.next()) {
+            const uint32_t n_it = it++;
+            if (static_cast<int>(n_it & 1) != g) continue;
+            const int j = walk.t * kWeighKeys + key;
+            const bool live = j < walk.P;
+            const long long at = static_cast<long long>(walk.unit) * cap + j;
+            float sum = 0.f, before = 0.f;
+            bool backed = false;
+            if (live) {
+                before = __ldcg(p.weight + at);
+                backed = p.pages.page_of(walk.b, j) >= 0;
+            }
+            if (walk.unit != have) {
+                have = walk.unit;
+                __syncwarp();  // the last unit's values have been read
+                for (int c = lane; c < n16; c += 32) {
+                    const float x = c < p.n ? __ldcg(p.lse + static_cast<long long>(have) * p.rows + p.row0 + c) : -INFINITY;
+                    lse2[c] = x == -INFINITY ? INFINITY : x * 1.4426950408889634f;  // such a row adds nothing
+                }
+                __syncwarp();
+            }
+            if (!wait_bar_warp(&s_full[g], (n_it >> 1) & 1, abort_flag, p.err)) break;
+            ptx::tc_fence_after();
+            for (int c0 = 0; c0 < n16; c0 += 16) {
+                uint32_t raw[16];
+                ptx::tmem_ld16(tmem + g * N + (static_cast<uint32_t>(32 * w) << 16) + c0, raw);
+                ptx::tmem_wait_ld();
+                ptx::reg_fence<16>(raw);
+                // columns past the last row hold another unit's query, or none: they add nothing whatever it is
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float e = ptx::ex2(__uint_as_float(raw[c]) * p.scale_log2 - lse2[c0 + c]);
+                    part[c & 3] += c0 + c < p.n ? e : 0.f;
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+            }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&s_free[g]);
+            if (live) p.weight_out[at] = before + (backed ? sum : 0.f);
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(done);
     }
 }
 

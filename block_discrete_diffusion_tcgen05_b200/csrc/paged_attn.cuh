@@ -167,29 +167,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attn_kernel(const __gr
     long long total, pos, end, ent_beg;
     int b, sgrid;
     {
-        const int per = (p.batch + kPagedThreads - 1) / kPagedThreads, b0 = tid * per;
-        long long mine = 0;
-        for (int i = b0; i < b0 + per && i < p.batch; ++i)
-            mine += static_cast<long long>(upe) * max(1, paged_chunks(ragged_clamp(__ldg(p.P_dev + i), cap), own_rows, CK));
-        long long inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (lane == 31) scan_sums[warp] = inc;
-        __syncthreads();
-        long long before = inc - mine;
-        total = 0;
-        for (int w = 0; w < kPagedThreads / 32; ++w) {
-            before += w < warp ? scan_sums[w] : 0;
-            total += scan_sums[w];
-        }
-        for (int i = b0; i < b0 + per && i < p.batch; ++i) {
-            pre[i] = before;
-            before += static_cast<long long>(upe) * max(1, paged_chunks(ragged_clamp(__ldg(p.P_dev + i), cap), own_rows, CK));
-        }
-        __syncthreads();
+        total = stream_prefix<kPagedThreads>(p.batch, pre, scan_sums, [&](int i) {
+            return static_cast<long long>(upe) * max(1, paged_chunks(ragged_clamp(__ldcg(p.P_dev + i), cap), own_rows, CK));
+        });
         // as many blocks as keep about kPagedMinChunks chunks each, one per unit at least, at most the grid
         long long g = total / kPagedMinChunks;
         const long long units = static_cast<long long>(p.batch) * upe;
@@ -199,13 +179,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attn_kernel(const __gr
         if (static_cast<int>(blockIdx.x) >= sgrid) return;
         pos = range_begin(blockIdx.x, total, sgrid);
         end = range_begin(blockIdx.x + 1, total, sgrid);
-        int lo = 0, hi = p.batch;  // pre[lo] <= pos < pre[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= pos) lo = mid;
-            else hi = mid;
-        }
-        b = lo;
+        b = stream_entry(pre, p.batch, pos);
         ent_beg = pre[b];
     }
 
@@ -222,7 +196,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attn_kernel(const __gr
 
     while (pos < end) {
         // ---- the unit: entry b, kv head h, query tile qt; its chunks [c0, c1) fall to this block
-        const int P = ragged_clamp(__ldg(p.P_dev + b), cap);
+        const int P = ragged_clamp(__ldcg(p.P_dev + b), cap);
         const int real = paged_chunks(P, own_rows, CK);
         const int Cu = max(1, real);
         const int u_in = static_cast<int>((pos - ent_beg) / Cu);
@@ -309,7 +283,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attn_kernel(const __gr
         // ---- the unit's query rows, rows past the last one zero
         for (int i = tid; i < ROWS * (D / 8); i += kPagedThreads) {
             const int r = i / (D / 8), u = i % (D / 8);
-            const uint4 x = r < rows_here ? __ldg(p.q + (row0 + r) * (D / 8) + u) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x = r < rows_here ? __ldcg(p.q + (row0 + r) * (D / 8) + u) : make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(smem + C::OFF_Q + (r / 16) * (16 * D * 2) + box_offset<D>(r % 16, u)) = x;
         }
         __syncthreads();
