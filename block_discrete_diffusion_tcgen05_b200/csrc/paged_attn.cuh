@@ -34,6 +34,7 @@ namespace e2d2 {
 
 constexpr int kPagedThreads = 128;
 constexpr int kPagedMaxCtas = 320;   // workspace sizing: tickets and partial slots
+constexpr int kPagedStats = 8192;    // row statistics of the parts of a unit that are joined at a time
 constexpr int kPagedMinChunks = 16;  // chunks per block that the split aims for
 
 struct alignas(64) PagedAttnParams {
@@ -77,7 +78,9 @@ struct PagedCfg {
     static constexpr int JOIN = KG * ROWS * RSTRIDE * 4;
     static constexpr int PRE = (kPagedMaxBatch + 1) * 8;    // prefix table of the schedule (in the ring)
     static constexpr int USED = KG * NST * STAGE;
-    static constexpr int RING_BYTES = ((USED > JOIN ? (USED > PRE ? USED : PRE) : (JOIN > PRE ? JOIN : PRE)) + 1023) / 1024 * 1024;
+    static constexpr int STATS = 2 * kPagedStats * 4;       // the join's row statistics (in the ring)
+    static constexpr int max2(int a, int b) { return a > b ? a : b; }
+    static constexpr int RING_BYTES = (max2(max2(USED, STATS), max2(JOIN, PRE)) + 1023) / 1024 * 1024;
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = RING_BYTES;
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;          // full[KG][NST], empty[KG][NST]
@@ -482,8 +485,11 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attn_kernel(const __gr
         __syncthreads();
         const int c_first = whole ? 0 : owner_cta(ubeg, total, sgrid);
         const int c_last = whole ? 0 : owner_cta(ubeg + Cu - 1, total, sgrid);
-        auto slot_of = [&](int c) {  // a block's last unit begins inside its range, its first one may not
-            return p.partial + static_cast<size_t>(range_begin(c, total, sgrid) >= ubeg ? 2 * c : 2 * c + 1) * p.slot_floats;
+        // A block's first unit takes its slot 2 c when it began before or at the block's range, a unit that begins
+        // inside the range takes 2 c + 1: of a unit's blocks only the first can be the latter.
+        const bool inside = !whole && range_begin(c_first, total, sgrid) < ubeg;
+        auto slot_of = [&](int c) {
+            return p.partial + static_cast<size_t>(2 * c + (c == c_first && inside)) * p.slot_floats;
         };
         float* slot = whole ? nullptr : slot_of(blockIdx.x);
         for (int i = tid; i < rows_here * (D / 4); i += kPagedThreads) {
@@ -528,28 +534,75 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attn_kernel(const __gr
             __syncthreads();
             if (*bcast) {
                 __threadfence();
-                for (int i = tid; i < rows_here * (D / 4); i += kPagedThreads) {
-                    const int row = i / (D / 4), q4 = i % (D / 4);
-                    float mt = -INFINITY;
-                    for (int c = c_first; c <= c_last; ++c) mt = fmaxf(mt, __ldcg(slot_of(c) + p.rows_cap * D + row));
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float lt = 0.f;
-#pragma unroll 4
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const float* sl = slot_of(c);
-                        const float mc = __ldcg(sl + p.rows_cap * D + row), lc = __ldcg(sl + p.rows_cap * D + p.rows_cap + row);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(sl + row * D) + q4);
-                        const float f = mc == -INFINITY ? 0.f : ptx::ex2(mc - mt);
-                        acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
-                        lt += lc * f;
+                // The ring is free: row statistics of a few rows at a time in shared memory, [part][row], then
+                // the parts' rows from L2 with several loads in flight per thread.
+                const int parts = c_last - c_first + 1;
+                const int rp = min(rows_here, kPagedStats / parts);
+                float* fm = join;            // maxima, then factors 2^(m - max)
+                float* fl = join + kPagedStats;     // sums
+                for (int r0 = 0; r0 < rows_here; r0 += rp) {
+                    const int nr = min(rp, rows_here - r0);
+                    for (int i = tid; i < parts * nr; i += kPagedThreads) {
+                        const int c = i / nr, row = i - c * nr;
+                        const float* st = slot_of(c_first + c) + p.rows_cap * D + r0 + row;
+                        fm[i] = __ldcg(st);
+                        fl[i] = __ldcg(st + p.rows_cap);
                     }
-                    const float inv = lt > 0.f ? 1.f / lt : 0.f;
-                    uint2 w;
-                    w.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
-                    w.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
-                    *reinterpret_cast<uint2*>(p.out + (row0 + row) * D + q4 * 4) = w;
-                    if (q4 == 0 && p.lse != nullptr)
-                        p.lse[row0 + row] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                    __syncthreads();
+                    // eight lanes per row
+                    for (int i = tid; i < (nr * 8 + 31) / 32 * 32; i += kPagedThreads) {
+                        const int row = i >> 3, part = i & 7;
+                        float mt = -INFINITY, lt = 0.f;
+                        if (row < nr)
+                            for (int c = part; c < parts; c += 8) mt = fmaxf(mt, fm[c * nr + row]);
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+                        if (row < nr)
+                            for (int c = part; c < parts; c += 8) {
+                                const float mc = fm[c * nr + row];
+                                const float f = mc == -INFINITY ? 0.f : ptx::ex2(mc - mt);
+                                fm[c * nr + row] = f;
+                                lt += fl[c * nr + row] * f;
+                            }
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+                        if (row < nr && part == 0) {
+                            fl[row] = lt > 0.f ? 1.f / lt : 0.f;  // part 0's sum of this row: read above, by these lanes only
+                            if (p.lse != nullptr)
+                                p.lse[row0 + r0 + row] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                        }
+                    }
+                    __syncthreads();
+                    constexpr int IT = 4;
+                    const int items = nr * (D / 4);
+                    for (int i0 = tid; i0 < items; i0 += IT * kPagedThreads) {
+                        float4 acc[IT];
+#pragma unroll
+                        for (int k = 0; k < IT; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                        for (int c = 0; c < parts; ++c) {
+                            const float4* sl = reinterpret_cast<const float4*>(slot_of(c_first + c)) + r0 * (D / 4);
+#pragma unroll
+                            for (int k = 0; k < IT; ++k) {
+                                const int i = i0 + k * kPagedThreads;
+                                if (i >= items) continue;
+                                const float4 x = __ldcg(sl + i);
+                                const float f = fm[c * nr + i / (D / 4)];
+                                acc[k].x += x.x * f, acc[k].y += x.y * f, acc[k].z += x.z * f, acc[k].w += x.w * f;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < IT; ++k) {
+                            const int i = i0 + k * kPagedThreads;
+                            if (i >= items) continue;
+                            const float inv = fl[i / (D / 4)];
+                            uint2 w;
+                            w.x = ptx::pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
+                            w.y = ptx::pack_bf16x2(acc[k].z * inv, acc[k].w * inv);
+                            *reinterpret_cast<uint2*>(p.out + (row0 + r0) * D + i * 4) = w;
+                        }
+                    }
+                    __syncthreads();
                 }
             }
         }
