@@ -969,10 +969,10 @@ unsigned copy_blocks(long long items, const DeviceInfo* di) {
     return static_cast<unsigned>(blocks < 1 ? 1 : blocks);
 }
 
-template <int D, int MT, int RW>
+template <int D, int RW>
 e2d2_status launch_paged(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
-    using C = PagedCfg<D, MT, RW>;
-    auto kern = paged_attn_kernel<D, MT, RW>;
+    using C = PagedCfg<D, RW>;
+    auto kern = paged_attn_kernel<D, RW>;
     static thread_local int configured_dev = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -981,17 +981,38 @@ e2d2_status launch_paged(const PagedAttnParams& a, const DeviceInfo* di, cudaStr
             return E2D2_ERR_CUDA;
         configured_dev = dev;
     }
-    const int grid = 2 * di->sms < kPagedMaxCtas ? 2 * di->sms : kPagedMaxCtas;
-    return launch_pdl(kern, dim3(grid), dim3(kPagedThreads), C::ALLOC, stream, a) == cudaSuccess ? E2D2_OK
-                                                                                                 : E2D2_ERR_CUDA;
+    const int grid = C::CTAS * di->sms < kPagedMaxCtas ? C::CTAS * di->sms : kPagedMaxCtas;
+    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::ALLOC, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
+}
+
+// Largest power of two that divides a page, `most` at most: the rows of a box.
+int box_of(const e2d2_pages& pages, int most) {
+    int box = most;
+    if (pages.page_table)
+        while (pages.page_rows % box != 0) box /= 2;
+    return box;
+}
+
+// bf16 tensor [units][rows][D] whose boxes hold every column of box_rows rows: 4D, the row's column halves of 128
+// bytes (one, of all columns, at D <= 64) as a dimension, so that one copy fills both swizzled halves.
+bool map_rows(CUtensorMap* m, const void* base, int D, long long rows, long long units, int box_rows) {
+    const int rb = (D * 2 < 128) ? D * 2 : 128;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(rb / 2), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(D * 2 / rb), static_cast<cuuint64_t>(units)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rb), static_cast<cuuint64_t>(rows) * D * 2};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(rb / 2), static_cast<cuuint32_t>(box_rows),
+                         static_cast<cuuint32_t>(D * 2 / rb), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
 e2d2_status launch_paged_rows(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
-    if (a.rows <= 16) return launch_paged<D, 1, 1>(a, di, stream);
-    if (a.rows <= 32) return launch_paged<D, 2, 1>(a, di, stream);
-    if (a.rows <= 64) return launch_paged<D, 2, 2>(a, di, stream);
-    return launch_paged<D, 2, 4>(a, di, stream);
+    if (a.rows <= 16) return launch_paged<D, 1>(a, di, stream);
+    if (a.rows <= 32) return launch_paged<D, 2>(a, di, stream);
+    return launch_paged<D, 4>(a, di, stream);
 }
 
 template <int D, int N>
@@ -1027,7 +1048,7 @@ struct PagedLayout {
 PagedLayout paged_layout(const e2d2_dims& dims, int S) {
     PagedLayout w;
     const long long rows = static_cast<long long>(dims.q_heads / dims.kv_heads) * S;
-    w.rows_cap = static_cast<int>(rows < 128 ? rows : 128);
+    w.rows_cap = static_cast<int>(rows < kPagedMaxRows ? rows : kPagedMaxRows);
     w.slot_floats = (w.rows_cap * (dims.head_dim + 2) + 31) / 32 * 32;
     w.bytes = 2048 + static_cast<size_t>(2) * kPagedMaxCtas * w.slot_floats * sizeof(float);
     return w;
@@ -1074,10 +1095,16 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     const long long BHkv = static_cast<long long>(dims.batch) * dims.kv_heads;
     PagedAttnParams a;
     const long long units = static_cast<long long>(pages.num_pages) * dims.kv_heads;
-    bool ok = map_3d(&a.tm_k, k_pages, D, pages.page_rows, units, pages.page_rows, 16) &&
-              map_3d(&a.tm_v, v_pages, D, pages.page_rows, units, pages.page_rows, 16);
+    a.rows = dims.q_heads / dims.kv_heads * S;
+    const int rw = a.rows <= 16 ? 1 : (a.rows <= 32 ? 2 : 4);
+    const int keys = (D == 128 ? 64 : 128) / rw;  // of a stage
+    a.box_rows = box_of(pages, keys);
+    a.own_box = 16;
+    while (a.own_box < S && a.own_box < keys) a.own_box *= 2;
+    bool ok = map_rows(&a.tm_k, k_pages, D, pages.page_rows, units, a.box_rows) &&
+              map_rows(&a.tm_v, v_pages, D, pages.page_rows, units, a.box_rows);
     if (ok && k_blk)
-        ok = map_3d(&a.tm_k1, k_blk, D, S, BHkv, S, 16) && map_3d(&a.tm_v1, v_blk, D, S, BHkv, S, 16);
+        ok = map_rows(&a.tm_k1, k_blk, D, S, BHkv, a.own_box) && map_rows(&a.tm_v1, v_blk, D, S, BHkv, a.own_box);
     if (!ok) return E2D2_ERR_CUDA;
     if (!k_blk) a.tm_k1 = a.tm_k, a.tm_v1 = a.tm_v;
     a.pages = page_view(pages, dims, di);
@@ -1093,8 +1120,7 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     a.group = dims.q_heads / dims.kv_heads;
     a.S = S;
     a.own = k_blk != nullptr;
-    a.rows = a.group * S;
-    a.qtiles = (a.rows + 127) / 128;
+    a.qtiles = (a.rows + kPagedMaxRows - 1) / kPagedMaxRows;
     a.rows_cap = w.rows_cap;
     a.slot_floats = w.slot_floats;
     a.scale_log2 = scale_log2(dims);
@@ -1160,10 +1186,7 @@ e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages p
     if (s != E2D2_OK) return s;
     const int D = dims.head_dim;
     const int rows = dims.q_heads / dims.kv_heads * S;
-    // boxes of the largest power of two rows, 128 at most, that divides a page
-    int box = 128;
-    if (pages.page_table)
-        while (pages.page_rows % box != 0) box /= 2;
+    const int box = box_of(pages, kWeighKeys);
     WeighParams a;
     if (!map_3d(&a.tm_k, k_pages, D, pages.page_rows, static_cast<long long>(pages.num_pages) * dims.kv_heads,
                 pages.page_rows, box) ||

@@ -48,6 +48,17 @@ struct PageView {
     }
 };
 
+// wait_bar_warp for a pipeline's steady state, where most waits are short and one follows the other: a few sleeping
+// attempts (the thread wakes when the phase completes, or after 50 us) before the bounded wait, whose limit and
+// clock cost a trip to global memory -- paid at every stage, that trip alone held a loader to one stage a
+// microsecond.
+__device__ __forceinline__ bool wait_stage_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+    bool ok = ptx::mbar_try_wait(bar, parity);
+    for (int i = 0; i < 4 && !ok; ++i) ok = ptx::mbar_try_wait_sleep(bar, parity, 50000u);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return wait_bar_warp(bar, parity, abort_flag, err);
+}
+
 // The work of a call as one stream: entry b takes count(b) items.  Fills pre[0..batch-1] with the items before
 // each entry (shared memory, as is sums[THREADS / 32]) and returns the sum of all.  Every thread of a block of
 // THREADS calls it; pre is readable after it.

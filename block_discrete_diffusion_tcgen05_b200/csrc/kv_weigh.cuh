@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             more = look_up();
             if (cu != have) {
                 const uint32_t qb = units % C::QB;
-                ok = wait_bar_warp(&q_empty[qb], ((units / C::QB) & 1) ^ 1, abort_flag, p.err);
+                ok = wait_stage_warp(&q_empty[qb], ((units / C::QB) & 1) ^ 1, abort_flag, p.err);
                 if (!ok) break;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(&q_full[qb], n16 * D * 2);
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
                 have = cu;
             }
             const uint32_t st = it % C::NST;
-            ok = wait_bar_warp(&k_empty[st], ((it / C::NST) & 1) ^ 1, abort_flag, p.err);
+            ok = wait_stage_warp(&k_empty[st], ((it / C::NST) & 1) ^ 1, abort_flag, p.err);
             if (!ok) break;
             const int n = __popc(__ballot_sync(0xffffffffu, cy >= 0));
             if (lane == 0) ptx::mbar_arrive_expect_tx(&k_full[st], static_cast<uint32_t>(n) * p.box_rows * D * 2);
@@ -229,13 +229,13 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             if (walk.unit != have) {
                 if (have >= 0 && leader) ptx::mma_commit(&q_empty[(units - 1) % C::QB]);
                 __syncwarp();
-                ok = wait_bar_warp(&q_full[units % C::QB], (units / C::QB) & 1, abort_flag, p.err);
+                ok = wait_stage_warp(&q_full[units % C::QB], (units / C::QB) & 1, abort_flag, p.err);
                 ++units;
                 have = walk.unit;
             }
             const uint32_t st = it % C::NST, sb = it & 1;
-            ok = ok && wait_bar_warp(&s_free[sb], ((it >> 1) & 1) ^ 1, abort_flag, p.err) &&
-                 wait_bar_warp(&k_full[st], (it / C::NST) & 1, abort_flag, p.err);
+            ok = ok && wait_stage_warp(&s_free[sb], ((it >> 1) & 1) ^ 1, abort_flag, p.err) &&
+                 wait_stage_warp(&k_full[st], (it / C::NST) & 1, abort_flag, p.err);
             if (!ok) break;
             ptx::tc_fence_after();
             if (leader) {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
                 }
                 __syncwarp();
             }
-            if (!wait_bar_warp(&s_full[g], (n_it >> 1) & 1, abort_flag, p.err)) break;
+            if (!wait_stage_warp(&s_full[g], (n_it >> 1) & 1, abort_flag, p.err)) break;
             ptx::tc_fence_after();
             for (int c0 = 0; c0 < n16; c0 += 16) {
                 uint32_t raw[16];
