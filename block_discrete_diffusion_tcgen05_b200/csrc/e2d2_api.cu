@@ -1101,14 +1101,14 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     a.box_rows = box_of(pages, keys);
     a.own_box = 16;
     while (a.own_box < S && a.own_box < keys) a.own_box *= 2;
-    bool ok = map_rows(&a.tm_k, k_pages, D, pages.page_rows, units, a.box_rows) &&
+    bool ok = map_rows(&a.tm_q, q_blk, D, static_cast<long long>(dims.batch) * dims.q_heads * S, 1, 16 * rw) &&
+              map_rows(&a.tm_k, k_pages, D, pages.page_rows, units, a.box_rows) &&
               map_rows(&a.tm_v, v_pages, D, pages.page_rows, units, a.box_rows);
     if (ok && k_blk)
         ok = map_rows(&a.tm_k1, k_blk, D, S, BHkv, a.own_box) && map_rows(&a.tm_v1, v_blk, D, S, BHkv, a.own_box);
     if (!ok) return E2D2_ERR_CUDA;
     if (!k_blk) a.tm_k1 = a.tm_k, a.tm_v1 = a.tm_v;
     a.pages = page_view(pages, dims, di);
-    a.q = static_cast<const uint4*>(q_blk);
     a.P_dev = P_dev;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;

@@ -41,8 +41,8 @@ constexpr int kPagedMinKeys = 256;  // keys per block that the split aims for
 struct alignas(64) PagedAttnParams {
     CUtensorMap tm_k, tm_v;    // pools: 4D {D half, page_rows, halves, num_pages * Hkv}, boxes of box_rows
     CUtensorMap tm_k1, tm_v1;  // own block, the same over {.., S, .., B * Hkv}, boxes of own_box
+    CUtensorMap tm_q;          // queries: the same over {.., B * Hq * S, .., 1}, boxes of a unit's rows
     PageView pages;
-    const uint4* q;            // [B][Hq][S][D] bf16
     const int* P_dev;
     __nv_bfloat16* out;        // [B][Hq][S][D]
     float* lse;                // [B][Hq][S] or null
@@ -83,8 +83,8 @@ struct PagedCfg {
     static_assert(SLICES * ROWS * RSTRIDE * 4 <= RING, "the ring holds the join");
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = RING;
-    static constexpr int OFF_BAR = OFF_Q + Q_BYTES;         // full[NST], empty[NST]
-    static constexpr int OFF_BAD = OFF_BAR + 2 * NST * 8;   // int [NST]: groups of 16 keys that no page backs
+    static constexpr int OFF_BAR = OFF_Q + Q_BYTES;         // full[NST], empty[NST], q_full
+    static constexpr int OFF_BAD = OFF_BAR + (2 * NST + 1) * 8;   // int [NST]: groups of 16 keys that no page backs
     static constexpr int OFF_STAT = (OFF_BAD + NST * 4 + 15) / 16 * 16;  // float m[SLICES][ROWS], l[SLICES][ROWS]
     static constexpr int OFF_MISC = OFF_STAT + 2 * SLICES * ROWS * 4;    // abort, broadcast
     static constexpr int ALLOC = OFF_MISC + 16 + 1024;      // + alignment slack
@@ -180,6 +180,11 @@ __device__ __forceinline__ int paged_parts(long long total, long long units, boo
     return static_cast<int>(want);
 }
 
+template <int V>
+struct Const {
+    static constexpr int value = V;
+};
+
 // m, l, acc += another part of the same row.
 __device__ __forceinline__ void join_part(float& m, float& l, float4& acc, float mc, float lc, const float4& x) {
     const float mn = fmaxf(m, mc);
@@ -212,6 +217,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     const bool loads = warp == C::WARPS;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* empty = full + NST;
+    uint64_t* q_full = empty + NST;
     volatile int* bad = reinterpret_cast<volatile int*>(smem + C::OFF_BAD);
     float* stat_m = reinterpret_cast<float*>(smem + C::OFF_STAT);
     float* stat_l = stat_m + SLICES * ROWS;
@@ -224,10 +230,12 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
             ptx::mbar_init(&full[i], 1);
             ptx::mbar_init(&empty[i], C::WARPS);
         }
+        ptx::mbar_init(q_full, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
     if (loads && lane == 0) {
+        ptx::tma_prefetch_desc(&p.tm_q);
         ptx::tma_prefetch_desc(&p.tm_k);
         ptx::tma_prefetch_desc(&p.tm_v);
     }
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     auto slice_base = [&](int box) { return static_cast<uint32_t>(key0 / box * (box * D * 2) + key0 % box * C::RB); };
     const uint32_t base_pool = slice_base(p.box_rows), base_own = slice_base(p.own_box);
     constexpr int SPC = C::RB / 32;  // steps per column chunk
-    uint32_t it = 0;                 // stages that went through the ring so far
+    uint32_t it = 0, n_units = 0;    // stages that went through the ring so far, units
 
     while (pos < end) {
         // ---- the unit: entry b, kv head h, query tile qt; its stages [c0, c1) fall to this block
@@ -315,6 +323,13 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
 
         if (loads) {
             // ------------------------------------------------------------ loads
+            // The unit's query rows come first, ahead of the stages that would fill the memory pipe.  Rows past the
+            // unit's last are other units' (or zeros): no row's result depends on another row.
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+                tma_load_4d(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(row0), 0);
+            }
+            __syncwarp();
             // A batch of 32 look-ups, NB of each stage: cur covers the stages being issued, nxt those after.
             constexpr int NB = KEYS / 16, SPB = 32 / NB;
             const int z_none = p.pages.num_pages * Hkv;  // past the pool: zeros are loaded
@@ -368,26 +383,20 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 __syncwarp();
                 if (++st == NST) st = 0, ++use;
             }
-            // every load has landed before the ring is used for anything else, timed out or not
+            // every load has landed before shared memory is used for anything else, timed out or not
             volatile int no_abort = 0;
             for (int k = i > NST ? i - NST : 0; k < i; ++k)
                 wait_bar_warp(&full[(it + k) % NST], ((it + k) / NST) & 1, &no_abort, p.err, true);
+            wait_bar_warp(q_full, n_units & 1, &no_abort, p.err, true);
         } else {
             // ------------------------------------------------------------ consumers
-            // the unit's query rows, rows past the last one zero
-            for (int x = tid; x < ROWS * (D / 8); x += NCONS) {
-                const int r = x / (D / 8), u = x % (D / 8);
-                const uint4 v = r < rows_here ? __ldcg(p.q + (row0 + r) * (D / 8) + u) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(smem + C::OFF_Q + tile_offset<D>(r, u, C::QCHUNK)) = v;
-            }
-            ptx::named_barrier_sync(1, NCONS);
-
+            const bool q_ok = wait_stage_warp(q_full, n_units & 1, abort_flag, p.err);
             float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
             for (int x = 0; x < NT; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
 
             uint32_t st = it % NST, use = it / NST;
-            for (int i = 0; i < n; ++i) {
+            for (int i = 0; i < n && q_ok; ++i) {
                 if (!wait_stage_warp(&full[st], use & 1, abort_flag, p.err)) break;
                 const int c = c0 + i;
                 const bool is_own = c < n_own;
@@ -561,36 +570,57 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                     const int parts = c_last - c_first + 1, items = rows_here * (D / 4);
                     int groups = 1;
                     while (2 * groups * items <= NCONS && 4 * groups <= parts) groups *= 2;
-                    float4* g_acc = reinterpret_cast<float4*>(smem + C::OFF_RING);  // [groups][items]
-                    float2* g_ml = reinterpret_cast<float2*>(smem + C::OFF_RING + NCONS * 16);
-                    for (int x = tid; x < groups * items; x += NCONS) {
-                        const int grp = x / items, i = x - grp * items;
-                        const int row = i / (D / 4), q4 = i % (D / 4);
-                        float mt = -INFINITY, lt = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const int first = c_first + grp * parts / groups, past = c_first + (grp + 1) * parts / groups;
-                        for (int c = first; c < past; c += 4) {
-                            float mc[4], lc[4];
-                            float4 v[4];
+                    // Joins parts [first, past) of IT items, NCONS apart, PB parts a trip to L2.
+                    auto join_items = [&](auto it_, auto pb_, int i0, int first, int past, float4* acc, float* mt, float* lt) {
+                        constexpr int IT = decltype(it_)::value, PB = decltype(pb_)::value;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                        for (int y = 0; y < IT; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f), mt[y] = -INFINITY, lt[y] = 0.f;
+#pragma unroll 1
+                        for (int c = first; c < past; c += PB) {
+                            float mc[PB][IT], lc[PB][IT];
+                            float4 v[PB][IT];
+#pragma unroll
+                            for (int k = 0; k < PB; ++k) {
                                 const bool in = c + k < past;
                                 const float* sl = slot_of(in ? c + k : c);
-                                mc[k] = in ? __ldcg(sl + p.rows_cap * D + row) : -INFINITY;
-                                lc[k] = __ldcg(sl + p.rows_cap * D + p.rows_cap + row);
-                                v[k] = __ldcg(reinterpret_cast<const float4*>(sl + row * D) + q4);
+#pragma unroll
+                                for (int y = 0; y < IT; ++y) {
+                                    const int i = min(i0 + y * NCONS, items - 1);
+                                    mc[k][y] = in ? __ldcg(sl + p.rows_cap * D + i / (D / 4)) : -INFINITY;
+                                    lc[k][y] = __ldcg(sl + p.rows_cap * D + p.rows_cap + i / (D / 4));
+                                    v[k][y] = __ldcg(reinterpret_cast<const float4*>(sl) + i);
+                                }
                             }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) join_part(mt, lt, acc, mc[k], lc[k], v[k]);
+                            for (int k = 0; k < PB; ++k)
+#pragma unroll
+                                for (int y = 0; y < IT; ++y) join_part(mt[y], lt[y], acc[y], mc[k][y], lc[k][y], v[k][y]);
                         }
-                        if (groups == 1) {
-                            write_row4(p, row0 + row, D, q4, mt, lt, acc);
-                        } else {
-                            g_acc[x] = acc;
-                            g_ml[x] = make_float2(mt, lt);
+                    };
+                    if (groups == 1) {
+                        constexpr int IT = 4;
+                        for (int i0 = tid; i0 < items; i0 += IT * NCONS) {
+                            float4 acc[IT];
+                            float mt[IT], lt[IT];
+                            join_items(Const<IT>(), Const<2>(), i0, c_first, c_last + 1, acc, mt, lt);
+#pragma unroll
+                            for (int y = 0; y < IT; ++y) {
+                                const int i = i0 + y * NCONS;
+                                if (i < items) write_row4(p, row0 + i / (D / 4), D, i % (D / 4), mt[y], lt[y], acc[y]);
+                            }
                         }
-                    }
-                    if (groups > 1) {  // then groups * items <= NCONS
+                    } else {  // groups * items <= NCONS
+                        float4* g_acc = reinterpret_cast<float4*>(smem + C::OFF_RING);  // [groups][items]
+                        float2* g_ml = reinterpret_cast<float2*>(smem + C::OFF_RING + NCONS * 16);
+                        if (tid < groups * items) {
+                            const int grp = tid / items;
+                            float4 acc;
+                            float mt, lt;
+                            join_items(Const<1>(), Const<8>(), tid - grp * items, c_first + grp * parts / groups,
+                                       c_first + (grp + 1) * parts / groups, &acc, &mt, &lt);
+                            g_acc[tid] = acc;
+                            g_ml[tid] = make_float2(mt, lt);
+                        }
                         ptx::named_barrier_sync(1, NCONS);
                         if (tid < items) {
                             float mt = -INFINITY, lt = 0.f;
@@ -606,6 +636,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
             }
         }
         it += n;
+        ++n_units;
         pos = ubeg + c1;
         if (u_in + 1 == upe && c1 == Cu) {
             ent_beg += static_cast<long long>(upe) * Cu;
