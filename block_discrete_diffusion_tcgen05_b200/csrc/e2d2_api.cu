@@ -1082,6 +1082,12 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     s = check_pages(pages, dims);
     if (s != E2D2_OK) return s;
     if (static_cast<long long>(dims.batch) * dims.q_heads * S > kMaxI32 / 8) return E2D2_ERR_SHAPE;
+    {
+        // every stage index of the stream fits in 31 bits
+        const long long rows = static_cast<long long>(dims.q_heads / dims.kv_heads) * S;
+        const long long units = static_cast<long long>(dims.batch) * dims.kv_heads * ((rows + kPagedMaxRows - 1) / kPagedMaxRows);
+        if (units * (row_capacity(pages) / 16 + S / 16 + 2 + kPagedUnitStages) > kMaxI32) return E2D2_ERR_SHAPE;
+    }
     if (!aligned16(q_blk) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_blk) || !aligned16(v_blk) ||
         !aligned16(out) || !aligned4(lse) || !aligned4(P_dev))
         return E2D2_ERR_ALIGNMENT;

@@ -28,11 +28,14 @@ struct PageView {
 
     __device__ __forceinline__ int capacity() const { return max_pages * page_rows; }
 
-    // Page that holds row r of entry b (r inside the capacity); -1, with the error recorded, if the
-    // table names no page of the pool.  Nothing is read or written through such an entry.
-    __device__ __forceinline__ int page_of(int b, int r) const {
+    // Page that holds row r of entry b (r inside the capacity), and the row inside it; -1, with the error recorded,
+    // if the table names no page of the pool.  Nothing is read or written through such an entry.
+    __device__ __forceinline__ int locate(int b, int r, int& in_page) const {
+        in_page = r;
         if (table == nullptr) return b;
-        const int pg = __ldcg(table + static_cast<size_t>(b) * max_pages + r / page_rows);
+        const int at = static_cast<unsigned>(r) / static_cast<unsigned>(page_rows);
+        in_page = r - at * page_rows;
+        const int pg = __ldcg(table + static_cast<size_t>(b) * max_pages + at);
         if (static_cast<unsigned>(pg) < static_cast<unsigned>(num_pages)) return pg;
         atomicOr(err, kErrBadPage);
         return -1;
@@ -41,10 +44,9 @@ struct PageView {
     // Row of the pool (in rows of d elements) that holds row r of entry b, head h; -1 as above.  64 bits:
     // a pool has more elements than 32 bits count.
     __device__ __forceinline__ long long pool_row(int b, int h, int r) const {
-        const int pg = page_of(b, r);
-        if (pg < 0) return -1;
-        const int in_page = table == nullptr ? r : r % page_rows;
-        return (static_cast<long long>(pg) * kv_heads + h) * page_rows + in_page;
+        int in_page;
+        const int pg = locate(b, r, in_page);
+        return pg < 0 ? -1 : (static_cast<long long>(pg) * kv_heads + h) * page_rows + in_page;
     }
 };
 

@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             const int r = walk.t * kWeighKeys + lane * p.box_rows;
             y = -1;
             if (lane < boxes && r < walk.P) {
-                const int pg = p.pages.page_of(walk.b, r);
-                y = p.pages.table == nullptr ? r : r % p.pages.page_rows;
+                const int pg = p.pages.locate(walk.b, r, y);
                 z = pg < 0 ? p.pages.num_pages * Hkv : (p.pages.table == nullptr ? unit : pg * Hkv + unit % Hkv);
             }
             return true;
@@ -276,7 +275,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             bool backed = false;
             if (live) {
                 before = __ldcg(p.weight + at);
-                backed = p.pages.page_of(walk.b, j) >= 0;
+                int in_page;
+                backed = p.pages.locate(walk.b, j, in_page) >= 0;
             }
             if (walk.unit != have) {
                 have = walk.unit;

@@ -22,8 +22,10 @@
 // more, they add nothing to the rounding of the output, for tensor-core time that the loads hide.
 //
 // The stages of all units form one stream that is cut evenly over the blocks (lengths are read on the device,
-// so any mix of lengths is balanced); a unit that several blocks share is joined by the last of them, from
-// fp32 partial results in the workspace, in the blocks' order.
+// so any mix of lengths is balanced); where lengths differ a unit takes kPagedUnitStages empty places ahead of its
+// stages, so that a block with many short units does not take as many stages as the others on top.  A unit that
+// several blocks share is joined by the last of them, from fp32 partial results in the workspace, in the blocks'
+// order.
 #pragma once
 
 #include <cstdint>
@@ -36,6 +38,7 @@ namespace e2d2 {
 
 constexpr int kPagedMaxCtas = 480;  // workspace sizing: tickets and partial slots
 constexpr int kPagedMaxRows = 64;   // query rows of a unit
+constexpr int kPagedUnitStages = 4; // what beginning and joining a unit costs, in stages, where lengths differ
 constexpr int kPagedMinKeys = 256;  // keys per block that the split aims for
 
 struct alignas(64) PagedAttnParams {
@@ -115,8 +118,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -136,29 +138,23 @@ __device__ __forceinline__ int paged_stages(int P, int own_rows, int keys) {
     return (own_rows + keys - 1) / keys + (P + keys - 1) / keys;
 }
 
-// 64-bit quotient of values that almost always fit in 32 bits.
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-    if (((a | b) >> 31) == 0) return static_cast<int>(a) / static_cast<int>(b);
-    return a / b;
-}
-
-// A stream of `total` items cut over `parts` blocks: block c takes [begin(c), begin(c + 1)), begin(c) =
-// floor(c total / parts).
+// A stream of `total` stages (below 2^31, the host sees to it) cut over `parts` blocks: block c takes
+// [begin(c), begin(c + 1)), begin(c) = floor(c total / parts).
 struct StreamCut {
-    long long total, q;
-    int parts, r;
-    __device__ StreamCut(long long t, int n) : total(t), parts(n) {
-        q = div_ll(t, n);
-        r = static_cast<int>(t - q * n);
+    unsigned total, q, r;
+    int parts;
+    __device__ StreamCut(unsigned t, int n) : total(t), q(t / n), r(t % n), parts(n) {}
+    __device__ unsigned begin(unsigned c) const { return c * q + (c * r) / parts; }  // c r < parts^2
+    // begin(c) <= x, without the division
+    __device__ bool begins_by(int c, unsigned x) const {
+        return static_cast<unsigned long long>(c) * total < (x + 1ull) * parts;
     }
-    __device__ long long begin(int c) const { return c * q + (c * r) / parts; }  // c r < parts^2
-    // The block that holds item x: an estimate, then the neighbours (the estimate is off by less than one
-    // block: 2^-23 of at most kPagedMaxCtas).
-    __device__ int owner(long long x) const {
-        int c = static_cast<int>(static_cast<float>(x) / static_cast<float>(total) * parts);
+    // The block that holds stage x: an estimate (off by less than one block), then its neighbours.
+    __device__ int owner(unsigned x) const {
+        int c = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(total)) * parts);
         c = max(0, min(c, parts - 1));
-        while (c > 0 && begin(c) > x) --c;
-        while (c + 1 < parts && begin(c + 1) <= x) ++c;
+        while (!begins_by(c, x)) --c;
+        while (c + 1 < parts && begins_by(c + 1, x)) ++c;
         return c;
     }
 };
@@ -166,42 +162,107 @@ struct StreamCut {
 // Blocks that a call's stream is cut over: as many as keep about kPagedMinKeys keys each, one per unit at least, at
 // most the grid.  Units of equal length are cut into equal parts each, if that leaves no more than a fifth of the
 // blocks idle: a block whose range meets two units joins twice.
-__device__ __forceinline__ int paged_parts(long long total, long long units, bool equal, int grid, int keys) {
-    long long want = total / (kPagedMinKeys / keys);
-    if (want < units) want = units;
+__device__ __forceinline__ int paged_parts(unsigned total, unsigned units, bool equal, unsigned grid, int keys) {
+    const unsigned want = max(total / (kPagedMinKeys / keys), units);
     if (want >= grid) {
         if (equal && units <= grid) {
-            const int per = grid / static_cast<int>(units), aligned = per * static_cast<int>(units);
+            const unsigned aligned = grid - grid % units;
             if (5 * aligned >= 4 * grid) return aligned;
         }
         return grid;
     }
-    if (equal) want -= want % units;
-    return static_cast<int>(want);
+    return equal ? want - want % units : want;
 }
 
-template <int V>
-struct Const {
-    static constexpr int value = V;
-};
-
-// m, l, acc += another part of the same row.
-__device__ __forceinline__ void join_part(float& m, float& l, float4& acc, float mc, float lc, const float4& x) {
-    const float mn = fmaxf(m, mc);
-    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - mn), f = mc == -INFINITY ? 0.f : ptx::ex2(mc - mn);
-    acc.x = acc.x * a + x.x * f, acc.y = acc.y * a + x.y * f, acc.z = acc.z * a + x.z * f, acc.w = acc.w * a + x.w * f;
-    l = l * a + lc * f;
-    m = mn;
-}
-
-__device__ __forceinline__ void write_row4(const PagedAttnParams& p, long long at, int D, int q4, float m, float l,
-                                           const float4& acc) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing: zeros, lse = -inf
+// Four columns of an output row from their weighted sum and the sum of the weights.
+__device__ __forceinline__ void write_row4(const PagedAttnParams& p, long long at, int D, int q4, float l, const float4& acc) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing: zeros
     uint2 w;
     w.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
     w.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(p.out + at * D + q4 * 4) = w;
-    if (q4 == 0 && p.lse != nullptr) p.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// The last block of a shared unit: joins its parts, in the blocks' order, and writes the rows.  The first part's
+// slot, then one every two slots from `rest`.  D / 4 lanes per row, four columns each, IT rows and AT parts in flight;
+// lane k of a row's lanes takes part k's maximum and sum.  No shared memory, no barrier.
+template <int D, int IT, int AT>
+__device__ __forceinline__ void join_parts(const PagedAttnParams& p, const float* first, const float* rest, int parts,
+                                           long long row0, int rows, int warp, int lane) {
+    constexpr int LPR = D / 4, RPW = 32 / LPR;
+    const int li = lane % LPR;
+    auto part = [&](int k) { return k == 0 ? first : rest + static_cast<size_t>(2 * (k - 1)) * p.slot_floats; };
+#pragma unroll 1
+    for (int base = warp * RPW; base < rows; base += 4 * RPW * IT) {
+        int row[IT];
+        float mt[IT], lt[IT];
+        float4 acc[IT];
+#pragma unroll
+        for (int y = 0; y < IT; ++y) {
+            row[y] = min(base + 4 * RPW * y + lane / LPR, rows - 1);
+            mt[y] = -INFINITY;
+            lt[y] = 0.f;
+            acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < parts; k0 += LPR) {  // as many parts as a row has lanes
+            const int np = min(LPR, parts - k0);
+            const float* st = part(k0 + min(li, np - 1)) + p.rows_cap * D;
+            float f[IT], lc[IT];
+            float4 x[AT][IT];
+#pragma unroll
+            for (int y = 0; y < IT; ++y) {
+                f[y] = li < np ? __ldcg(st + row[y]) : -INFINITY;
+                lc[y] = __ldcg(st + p.rows_cap + row[y]);
+            }
+#pragma unroll
+            for (int k = 0; k < AT; ++k)
+#pragma unroll
+                for (int y = 0; y < IT; ++y)
+                    x[k][y] = __ldcg(reinterpret_cast<const float4*>(part(k0 + min(k, np - 1)) + row[y] * D) + li);
+#pragma unroll
+            for (int y = 0; y < IT; ++y) {
+                float mn = f[y];
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mn = fmaxf(mn, mt[y]);
+                const float f_old = mt[y] == -INFINITY ? 0.f : ptx::ex2(mt[y] - mn);
+                f[y] = f[y] == -INFINITY ? 0.f : ptx::ex2(f[y] - mn);
+                float ls = li < np ? lc[y] * f[y] : 0.f;
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+                lt[y] = lt[y] * f_old + ls;
+                mt[y] = mn;
+                acc[y].x *= f_old, acc[y].y *= f_old, acc[y].z *= f_old, acc[y].w *= f_old;
+            }
+#pragma unroll 1
+            for (int k = 0; k < np; k += AT) {
+#pragma unroll
+                for (int z = 0; z < AT; ++z)
+#pragma unroll
+                    for (int y = 0; y < IT; ++y) {
+                        const float fk = __shfl_sync(0xffffffffu, f[y], (lane & ~(LPR - 1)) + min(k + z, LPR - 1));
+                        if (k + z < np) {
+                            acc[y].x += x[z][y].x * fk, acc[y].y += x[z][y].y * fk;
+                            acc[y].z += x[z][y].z * fk, acc[y].w += x[z][y].w * fk;
+                        }
+                    }
+                if (k + AT < np)
+#pragma unroll
+                    for (int z = 0; z < AT; ++z)
+#pragma unroll
+                        for (int y = 0; y < IT; ++y)
+                            x[z][y] = __ldcg(reinterpret_cast<const float4*>(part(k0 + min(k + AT + z, np - 1)) + row[y] * D) + li);
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < IT; ++y)
+            if (base + 4 * RPW * y + lane / LPR < rows) {
+                write_row4(p, row0 + row[y], D, li, lt[y], acc[y]);
+                if (li == 0 && p.lse != nullptr)
+                    p.lse[row0 + row[y]] = lt[y] > 0.f ? (mt[y] + log2f(lt[y])) * 0.69314718055994531f : -INFINITY;
+            }
+    }
 }
 
 template <int D, int RW>
@@ -252,38 +313,39 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
         P = base + lane < p.batch ? ragged_clamp(__ldcg(p.P_dev + base + lane), cap) : 0;
         stages = base + lane < p.batch ? max(1, paged_stages(P, own_rows, KEYS)) : 0;
     };
-    long long sum = 0;               // stages of one unit of every entry
-    unsigned most = 0;
+    unsigned sum = 0, most = 0;      // stages of one unit of every entry, of the longest
     for (int base = 0; base < p.batch; base += 32) {
         lane_entry(base);
         sum += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(stages));
         most = max(most, __reduce_max_sync(0xffffffffu, static_cast<unsigned>(stages)));
     }
-    const long long total = sum * upe;
-    const StreamCut cut(total, paged_parts(total, static_cast<long long>(p.batch) * upe,
-                                           sum == static_cast<long long>(most) * p.batch, gridDim.x, KEYS));
+    const bool equal = sum == most * p.batch;
+    const unsigned lead = equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
+    const unsigned total = (sum + lead * p.batch) * upe;
+    const StreamCut cut(total, paged_parts(total, p.batch * upe, equal, gridDim.x, KEYS));
     if (static_cast<int>(blockIdx.x) >= cut.parts) return;
-    long long pos = cut.begin(blockIdx.x);
-    const long long end = cut.begin(blockIdx.x + 1);
+    unsigned pos = cut.begin(blockIdx.x);
+    const unsigned end = cut.begin(blockIdx.x + 1);
     int b = 0;
-    long long ent_beg = 0;
+    unsigned ent_beg = 0;
     for (int base = 0;; base += 32) {
         if (p.batch > 32) lane_entry(base);
-        unsigned inc = stages;
+        const unsigned places = stages > 0 ? stages + lead : 0;
+        unsigned inc = places;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, ent_beg + static_cast<long long>(inc) * upe > pos);
+        const unsigned past = __ballot_sync(0xffffffffu, ent_beg + inc * upe > pos);
         if (past != 0 || base + 32 >= p.batch) {
             const int at = past != 0 ? __ffs(past) - 1 : 31;
             b = base + at;
-            ent_beg += static_cast<long long>(__shfl_sync(0xffffffffu, inc - stages, at)) * upe;
+            ent_beg += __shfl_sync(0xffffffffu, inc - places, at) * upe;
             P = __shfl_sync(0xffffffffu, P, at);
             break;
         }
-        ent_beg += static_cast<long long>(__shfl_sync(0xffffffffu, inc, 31)) * upe;
+        ent_beg += __shfl_sync(0xffffffffu, inc, 31) * upe;
     }
     if (loads) test_producer_delay();
     __syncthreads();  // the barriers are initialised
@@ -310,14 +372,23 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
         // ---- the unit: entry b, kv head h, query tile qt; its stages [c0, c1) fall to this block
         const int real = paged_stages(P, own_rows, KEYS);
         const int Cu = max(1, real);
-        const int u_in = static_cast<int>(div_ll(pos - ent_beg, Cu));
-        const long long ubeg = ent_beg + static_cast<long long>(u_in) * Cu;
-        const int h = u_in / p.qtiles, qt = u_in - h * p.qtiles;
-        const int c0 = static_cast<int>(pos - ubeg);
-        const int c1 = static_cast<int>((end < ubeg + Cu ? end : ubeg + Cu) - ubeg);
+        const unsigned len = lead + Cu;
+        const int u_in = (pos - ent_beg) / len;
+        const unsigned ubeg = ent_beg + u_in * len, past = min(end - ubeg, len);
+        const int h = p.qtiles == 1 ? u_in : u_in / p.qtiles, qt = u_in - h * p.qtiles;
+        const int c0 = max(static_cast<int>(pos - ubeg - lead), 0), c1 = max(static_cast<int>(past - lead), 0);
         const bool whole = c0 == 0 && c1 == Cu;
+        pos = ubeg + past;
+        const int unit_b = b;
+        const int unit_P = P;
+        if (u_in + 1 == upe && past == len) {
+            ent_beg += upe * len;
+            ++b;
+            if (pos < end) P = ragged_clamp(__ldcg(p.P_dev + b), cap);
+        }
+        if (c0 == c1) continue;  // empty places only
         const int rows_here = min(ROWS, p.rows - qt * ROWS);
-        const long long row0 = (static_cast<long long>(b) * p.q_heads + static_cast<long long>(h) * p.group) * p.S +
+        const long long row0 = (static_cast<long long>(unit_b) * p.q_heads + static_cast<long long>(h) * p.group) * p.S +
                                static_cast<long long>(qt) * ROWS;
         const int n = max(0, min(c1, real) - c0);  // stages with keys
 
@@ -335,16 +406,15 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
             const int z_none = p.pages.num_pages * Hkv;  // past the pool: zeros are loaded
             auto look_up = [&](int i, int& y, int& z) {  // box lane % NB of stage i: first row, pool index
                 y = -1;
-                z = b * Hkv + h;
+                z = unit_b * Hkv + h;
                 const int c = c0 + i;
                 if (i >= n) return;
                 const int box = c < n_own ? p.own_box : p.box_rows, in = (lane % NB) * box;
                 const int r = (c < n_own ? c : c - n_own) * KEYS + in;
-                if (in >= KEYS || r >= (c < n_own ? own_rows : P)) return;
+                if (in >= KEYS || r >= (c < n_own ? own_rows : unit_P)) return;
                 y = r;
                 if (c >= n_own && p.pages.table != nullptr) {
-                    const int pg = p.pages.page_of(b, r);
-                    y = r % p.pages.page_rows;
+                    const int pg = p.pages.locate(unit_b, r, y);
                     z = pg < 0 ? z_none : pg * Hkv + h;
                 }
             };
@@ -401,16 +471,18 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 const int c = c0 + i;
                 const bool is_own = c < n_own;
                 // keys of this warp's slice that exist (any number, 0 and below for none)
-                const int valid = (is_own ? own_rows - c * KEYS : P - (c - n_own) * KEYS) - key0;
+                const int valid = (is_own ? own_rows - c * KEYS : unit_P - (c - n_own) * KEYS) - key0;
                 const int lost = (bad[st] >> (slice * SUB)) & ((1 << SUB) - 1);
                 if (valid > 0) {
                     const int half = (is_own ? p.own_box : p.box_rows) * C::RB;
                     const uint32_t sk = ring + st * C::STAGE + (is_own ? base_own : base_pool) + ok_;
                     const uint32_t sv = ring + st * C::STAGE + C::KB + (is_own ? base_own : base_pool) + ov_;
-                    // S = Q K^T
-                    float s[2 * SUB][4];
+                    // S = Q K^T, even and odd steps in accumulators of their own (shorter chains)
+                    float s[2 * SUB][4], s1[2 * SUB][4];
 #pragma unroll
-                    for (int x = 0; x < 2 * SUB; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+                    for (int x = 0; x < 2 * SUB; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[x][e] = s1[x][e] = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         uint32_t qa[4];
@@ -419,10 +491,14 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                         for (int sb = 0; sb < SUB; ++sb) {
                             uint32_t kb[4];
                             ldsm4((sk ^ ((ks % SPC) * 32)) + (ks / SPC) * half + sb * 16 * C::RB, kb);
-                            mma_16816(s[2 * sb], qa, kb[0], kb[1]);
-                            mma_16816(s[2 * sb + 1], qa, kb[2], kb[3]);
+                            mma_16816((ks & 1) ? s1[2 * sb] : s[2 * sb], qa, kb[0], kb[1]);
+                            mma_16816((ks & 1) ? s1[2 * sb + 1] : s[2 * sb + 1], qa, kb[2], kb[3]);
                         }
                     }
+#pragma unroll
+                    for (int x = 0; x < 2 * SUB; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[x][e] += s1[x][e];
                     // Keys past the end, and those that no page backs, get no weight; their V rows (anything, NaN
                     // included) must not meet the product with a zero probability, so they become zero.
                     if (valid < SK || lost != 0) {
@@ -479,17 +555,22 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                             ph[sb][e] = hi;
                             pl[sb][e] = ptx::pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
                         }
-                    // O += P V
+                    // O += P V, two column pairs at a time: a product and its remainder's are four apart
 #pragma unroll
                     for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
-                            uint32_t vb[4];
-                            ldsm4t((sv ^ ((j % SPC) * 32)) + (j / SPC) * half + sb * 16 * C::RB, vb);
-                            mma_16816(o[2 * j], ph[sb], vb[0], vb[1]);
-                            mma_16816(o[2 * j + 1], ph[sb], vb[2], vb[3]);
-                            mma_16816(o[2 * j], pl[sb], vb[0], vb[1]);
-                            mma_16816(o[2 * j + 1], pl[sb], vb[2], vb[3]);
+                        for (int j = 0; j < D / 16; j += 2) {
+                            uint32_t v0[4], v1[4];
+                            ldsm4t((sv ^ ((j % SPC) * 32)) + (j / SPC) * half + sb * 16 * C::RB, v0);
+                            ldsm4t((sv ^ (((j + 1) % SPC) * 32)) + ((j + 1) / SPC) * half + sb * 16 * C::RB, v1);
+                            mma_16816(o[2 * j], ph[sb], v0[0], v0[1]);
+                            mma_16816(o[2 * j + 1], ph[sb], v0[2], v0[3]);
+                            mma_16816(o[2 * j + 2], ph[sb], v1[0], v1[1]);
+                            mma_16816(o[2 * j + 3], ph[sb], v1[2], v1[3]);
+                            mma_16816(o[2 * j], pl[sb], v0[0], v0[1]);
+                            mma_16816(o[2 * j + 1], pl[sb], v0[2], v0[3]);
+                            mma_16816(o[2 * j + 2], pl[sb], v1[0], v1[1]);
+                            mma_16816(o[2 * j + 3], pl[sb], v1[2], v1[3]);
                         }
                 }
                 __syncwarp();
@@ -520,13 +601,9 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                     *reinterpret_cast<float2*>(dst + x * 8) = make_float2(o[x][2 * r] * f, o[x][2 * r + 1] * f);
             }
             ptx::named_barrier_sync(1, NCONS);
-            const int c_first = whole ? 0 : cut.owner(ubeg);
-            // A block's first unit takes its slot 2 c when it began before or at the block's range, a unit that
-            // begins inside the range takes 2 c + 1: of a unit's blocks only the first can be the latter.
-            const bool inside = !whole && cut.begin(c_first) < ubeg;
-            auto slot_of = [&](int c) {
-                return p.partial + static_cast<size_t>(2 * c + (c == c_first && inside)) * p.slot_floats;
-            };
+            const int c_first = whole ? 0 : cut.owner(ubeg + lead);
+            // A block begins one shared unit at most and goes on with one at most: a slot for each.
+            auto slot_of = [&](int c) { return p.partial + static_cast<size_t>(2 * c + (c == c_first)) * p.slot_floats; };
             float* slot = whole ? nullptr : slot_of(blockIdx.x);
             for (int x = tid; x < rows_here * (D / 4); x += NCONS) {
                 const int row = x / (D / 4), q4 = x % (D / 4);
@@ -542,7 +619,9 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                     for (int k = 0; k < SLICES; ++k) lt += stat_l[k * ROWS + row], mt = fmaxf(mt, stat_m[k * ROWS + row]);
                 }
                 if (whole) {
-                    write_row4(p, row0 + row, D, q4, mt, lt, acc);
+                    write_row4(p, row0 + row, D, q4, lt, acc);
+                    if (q4 == 0 && p.lse != nullptr)
+                        p.lse[row0 + row] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
                 } else {
                     __stcg(reinterpret_cast<float4*>(slot + row * D) + q4, acc);
                     if (q4 == 0) {
@@ -554,7 +633,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
             if (!whole) {
                 // publish; the last block of the unit joins all of them
                 ptx::named_barrier_sync(1, NCONS);
-                const int c_last = cut.owner(ubeg + Cu - 1);
+                const int c_last = cut.owner(ubeg + len - 1);
                 if (tid == 0) {
                     __threadfence();
                     const int ticket = atomicAdd(&p.tickets[c_first], 1);
@@ -565,84 +644,14 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 ptx::named_barrier_sync(1, NCONS);
                 if (*bcast) {
                     __threadfence();
-                    // Thread = (group of parts, row, four columns): few items leave threads for several groups,
-                    // which are joined in shared memory, in the groups' order.
-                    const int parts = c_last - c_first + 1, items = rows_here * (D / 4);
-                    int groups = 1;
-                    while (2 * groups * items <= NCONS && 4 * groups <= parts) groups *= 2;
-                    // Joins parts [first, past) of IT items, NCONS apart, PB parts a trip to L2.
-                    auto join_items = [&](auto it_, auto pb_, int i0, int first, int past, float4* acc, float* mt, float* lt) {
-                        constexpr int IT = decltype(it_)::value, PB = decltype(pb_)::value;
-#pragma unroll
-                        for (int y = 0; y < IT; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f), mt[y] = -INFINITY, lt[y] = 0.f;
-#pragma unroll 1
-                        for (int c = first; c < past; c += PB) {
-                            float mc[PB][IT], lc[PB][IT];
-                            float4 v[PB][IT];
-#pragma unroll
-                            for (int k = 0; k < PB; ++k) {
-                                const bool in = c + k < past;
-                                const float* sl = slot_of(in ? c + k : c);
-#pragma unroll
-                                for (int y = 0; y < IT; ++y) {
-                                    const int i = min(i0 + y * NCONS, items - 1);
-                                    mc[k][y] = in ? __ldcg(sl + p.rows_cap * D + i / (D / 4)) : -INFINITY;
-                                    lc[k][y] = __ldcg(sl + p.rows_cap * D + p.rows_cap + i / (D / 4));
-                                    v[k][y] = __ldcg(reinterpret_cast<const float4*>(sl) + i);
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < PB; ++k)
-#pragma unroll
-                                for (int y = 0; y < IT; ++y) join_part(mt[y], lt[y], acc[y], mc[k][y], lc[k][y], v[k][y]);
-                        }
-                    };
-                    if (groups == 1) {
-                        constexpr int IT = 4;
-                        for (int i0 = tid; i0 < items; i0 += IT * NCONS) {
-                            float4 acc[IT];
-                            float mt[IT], lt[IT];
-                            join_items(Const<IT>(), Const<2>(), i0, c_first, c_last + 1, acc, mt, lt);
-#pragma unroll
-                            for (int y = 0; y < IT; ++y) {
-                                const int i = i0 + y * NCONS;
-                                if (i < items) write_row4(p, row0 + i / (D / 4), D, i % (D / 4), mt[y], lt[y], acc[y]);
-                            }
-                        }
-                    } else {  // groups * items <= NCONS
-                        float4* g_acc = reinterpret_cast<float4*>(smem + C::OFF_RING);  // [groups][items]
-                        float2* g_ml = reinterpret_cast<float2*>(smem + C::OFF_RING + NCONS * 16);
-                        if (tid < groups * items) {
-                            const int grp = tid / items;
-                            float4 acc;
-                            float mt, lt;
-                            join_items(Const<1>(), Const<8>(), tid - grp * items, c_first + grp * parts / groups,
-                                       c_first + (grp + 1) * parts / groups, &acc, &mt, &lt);
-                            g_acc[tid] = acc;
-                            g_ml[tid] = make_float2(mt, lt);
-                        }
-                        ptx::named_barrier_sync(1, NCONS);
-                        if (tid < items) {
-                            float mt = -INFINITY, lt = 0.f;
-                            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int grp = 0; grp < groups; ++grp) {
-                                const float2 ml = g_ml[grp * items + tid];
-                                join_part(mt, lt, acc, ml.x, ml.y, g_acc[grp * items + tid]);
-                            }
-                            write_row4(p, row0 + tid / (D / 4), D, tid % (D / 4), mt, lt, acc);
-                        }
-                    }
+                    const int parts = c_last - c_first + 1;
+                    if (rows_here <= 2 * C::WARPS * (128 / D)) join_parts<D, 1, 8>(p, slot_of(c_first), slot_of(c_first + 1), parts, row0, rows_here, warp, lane);
+                    else join_parts<D, 4, 2>(p, slot_of(c_first), slot_of(c_first + 1), parts, row0, rows_here, warp, lane);
                 }
             }
         }
         it += n;
         ++n_units;
-        pos = ubeg + c1;
-        if (u_in + 1 == upe && c1 == Cu) {
-            ent_beg += static_cast<long long>(upe) * Cu;
-            ++b;
-            if (pos < end) P = ragged_clamp(__ldcg(p.P_dev + b), cap);
-        }
         ptx::fence_proxy_async_smem();  // the join's accesses to the ring come before the next loads
         __syncthreads();                // the join has been read, no wait is pending
         if (*abort_flag) return;
