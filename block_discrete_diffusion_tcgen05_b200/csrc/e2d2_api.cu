@@ -1055,6 +1055,22 @@ PagedLayout paged_layout(const e2d2_dims& dims, int S) {
 }
 static_assert(kPagedMaxCtas * sizeof(int) <= 2048, "tickets");
 
+template <int THREADS>
+e2d2_status launch_evict_select(const EvictParams& a, unsigned units, cudaStream_t stream) {
+    auto kern = kv_evict_select_kernel<THREADS>;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictRows * 4) != cudaSuccess)
+            return E2D2_ERR_CUDA;
+        configured_dev = dev;
+    }
+    return launch_pdl(kern, dim3(units), dim3(THREADS), static_cast<size_t>(a.rank_rows) * 4, stream, a) == cudaSuccess
+               ? E2D2_OK
+               : E2D2_ERR_CUDA;
+}
+
 // Rows that one list of an eviction can hold, rounded to whole 16 bytes.
 long long evict_list_rows(const e2d2_pages& pg) { return (row_capacity(pg) / 2 + 4) / 4 * 4; }
 
@@ -1265,13 +1281,22 @@ e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, 
     a.list_rows = static_cast<int>(evict_list_rows(pages));
     a.ws_stride = 4 + 2ll * a.list_rows;
     const unsigned units = static_cast<unsigned>(dims.batch) * dims.kv_heads;
-    if (launch_pdl(kv_evict_select_kernel, dim3(units), dim3(kEvictThreads), 0, stream, a) != cudaSuccess)
-        return E2D2_ERR_CUDA;
-    const long long most = static_cast<long long>(a.list_rows) * 2 * a.vec_per_row;  // thread-steps of a unit
-    unsigned x = (di->sms * 8 + units - 1) / units;
-    if (x > (most + 255) / 256) x = static_cast<unsigned>((most + 255) / 256);
-    return launch_pdl(kv_evict_move_kernel, dim3(x, units), dim3(256), 0, stream, a) == cudaSuccess ? E2D2_OK
-                                                                                                    : E2D2_ERR_CUDA;
+    const long long cap = row_capacity(pages);
+    a.rank_rows = static_cast<int>(cap < kEvictRows ? cap : kEvictRows);
+    s = cap <= 4096 ? launch_evict_select<256>(a, units, stream) : launch_evict_select<1024>(a, units, stream);
+    if (s != E2D2_OK) return s;
+    // eight moves per warp and round, at most eight blocks per SM
+    const long long most = (a.list_rows + 63) / 64;
+    long long x = (di->sms * 8 + units - 1) / units;
+    if (x > most) x = most;
+    const dim3 grid(static_cast<unsigned>(x), units);
+    cudaError_t e;
+    switch (dims.head_dim) {
+        case 32: e = launch_pdl(kv_evict_move_kernel<4>, grid, dim3(256), 0, stream, a); break;
+        case 64: e = launch_pdl(kv_evict_move_kernel<8>, grid, dim3(256), 0, stream, a); break;
+        default: e = launch_pdl(kv_evict_move_kernel<16>, grid, dim3(256), 0, stream, a); break;
+    }
+    return e == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
 }
 
 }  // extern "C"
