@@ -961,12 +961,10 @@ PageView page_view(const e2d2_pages& pg, const e2d2_dims& dims, const DeviceInfo
 
 long long row_capacity(const e2d2_pages& pg) { return static_cast<long long>(pg.max_pages) * pg.page_rows; }
 
-// Blocks of 256 threads for `items` thread-steps, at most eight per SM.
-unsigned copy_blocks(long long items, const DeviceInfo* di) {
-    long long blocks = (items + 255) / 256;
-    const long long cap = static_cast<long long>(di->sms) * 8;
-    if (blocks > cap) blocks = cap;
-    return static_cast<unsigned>(blocks < 1 ? 1 : blocks);
+// Blocks of eight warps for `rows` rows, eight a warp; at most eight blocks per SM.
+unsigned copy_blocks(long long rows, const DeviceInfo* di) {
+    const long long blocks = (rows + 63) / 64, most = static_cast<long long>(di->sms) * 8;
+    return static_cast<unsigned>(blocks < most ? (blocks < 1 ? 1 : blocks) : most);
 }
 
 template <int D, int RW>
@@ -1183,11 +1181,15 @@ e2d2_status e2d2_kv_cache_append_paged(void* k_pages, void* v_pages, e2d2_pages 
     a.tokens = tokens_dev;
     a.batch = dims.batch;
     a.S_new = S_new;
-    a.vec_per_row = dims.head_dim / 8;
-    const long long total = static_cast<long long>(dims.batch) * dims.kv_heads * S_new * a.vec_per_row;
-    return launch_pdl(kv_append_paged_kernel, dim3(copy_blocks(total, di), 2), dim3(256), 0, stream, a) == cudaSuccess
-               ? E2D2_OK
-               : E2D2_ERR_CUDA;
+    const long long total = static_cast<long long>(dims.batch) * dims.kv_heads * S_new;
+    const dim3 grid(copy_blocks(total, di));
+    cudaError_t e;
+    switch (dims.head_dim) {
+        case 32: e = launch_pdl(kv_append_paged_kernel<4>, grid, dim3(256), 0, stream, a); break;
+        case 64: e = launch_pdl(kv_append_paged_kernel<8>, grid, dim3(256), 0, stream, a); break;
+        default: e = launch_pdl(kv_append_paged_kernel<16>, grid, dim3(256), 0, stream, a); break;
+    }
+    return e == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
 }
 
 e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages pages, const int* P_dev,
@@ -1277,7 +1279,6 @@ e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, 
     a.batch = dims.batch;
     a.keep = keep;
     a.recent = recent;
-    a.vec_per_row = dims.head_dim / 8;
     a.list_rows = static_cast<int>(evict_list_rows(pages));
     a.ws_stride = 4 + 2ll * a.list_rows;
     const unsigned units = static_cast<unsigned>(dims.batch) * dims.kv_heads;

@@ -9,8 +9,8 @@
 //
 // Two launches: select (one block per (entry, kv head)) finds the kept rows and writes the lists of movers
 // and holes, move copies the K and V rows over the whole GPU.  Select reads 8 bytes a row once, keeps the rows'
-// ranks in shared memory (up to 32768 rows), finds the keep-th largest by its four bytes in turn (a histogram of 256
-// bins each) and turns "stays" into one bit a row, from whose counts every row's place in its list follows: no
+// ranks in shared memory (up to 32768 rows), finds the keep-th largest by 11, 11 and 10 bits in turn (histograms
+// in shared memory; eleven bits tell weights apart that share an exponent, so few lanes meet in a bin) and turns "stays" into one bit a row, from whose counts every row's place in its list follows: no
 // sort, and no atomics but the histograms' counts.
 #pragma once
 
@@ -33,7 +33,7 @@ struct EvictParams {
     int* pos_out;
     int* P_out;
     int* ws;              // per unit: count, kept length, 2 unused, then list_rows holes, list_rows movers
-    int batch, keep, recent, vec_per_row;
+    int batch, keep, recent;
     int list_rows;
     int rank_rows;        // rows that the launch's shared memory has ranks for
     long long ws_stride;
@@ -75,9 +75,9 @@ __device__ __forceinline__ int2 block_exclusive_scan(int x, int y, int2* wsum, i
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_constant__ EvictParams p) {
     constexpr int WARPS = THREADS / 32;
-    __shared__ unsigned int hist[256];
+    __shared__ unsigned int hist[2048];
     __shared__ int2 wsum[WARPS];
-    __shared__ unsigned int s_pick[3];                // leading bytes, rows of them that stay, rows that have them
+    __shared__ unsigned int s_pick[3];                // leading bits, rows of them that stay, rows that have them
     __shared__ uint32_t kept_bits[kEvictRows / 32];
     __shared__ int2 word_at[kEvictRows / 32];         // holes and movers before each 32 rows
     extern __shared__ uint32_t ranks[];               // [rank_rows]
@@ -109,50 +109,71 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
     const int protect = pf < INT_MIN ? INT_MIN : static_cast<int>(pf);
     const bool held = P <= p.rank_rows;
     auto rank_of = [&](int j) { return held ? ranks[j] : evict_rank(__ldcg(w + j), __ldcg(pos + j), protect); };
-    if (tid < 256) hist[tid] = 0;
-    for (int i = tid + THREADS; i < 256; i += THREADS) hist[i] = 0;
+    for (int i = tid; i < 2048; i += THREADS) hist[i] = 0;
     __syncthreads();
 
-    // The keep-th largest rank, a byte a pass: prefix = its leading bytes, need = how many rows with that prefix
-    // stay.  The first pass also fills the ranks.
+    // The keep-th largest rank, 11, 11 and 10 bits a pass: prefix = its leading bits, need = how many rows with that
+    // prefix stay.  The first pass also fills the ranks.
     unsigned int prefix = 0, need = p.keep, equal = 0;
+    auto count = [&](bool in, uint32_t bin) {
+        // equal weights (a fresh cache's zeros) would queue at one bin: a warp of one bin counts once
+        const unsigned int lanes = __ballot_sync(0xffffffffu, in);
+        if (lanes == 0) return;
+        const int lead = __ffs(lanes) - 1;
+        const uint32_t first = __shfl_sync(0xffffffffu, bin, lead);
+        if (__all_sync(0xffffffffu, !in || bin == first)) {
+            if (lane == lead) atomicAdd(&hist[bin], __popc(lanes));
+        } else if (in) {
+            atomicAdd(&hist[bin], 1u);
+        }
+    };
+    constexpr int BATCH = 8;
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int j0 = 0; j0 < P; j0 += BATCH * THREADS) {
+        float wv[BATCH];
+        int pv[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int j = j0 + k * THREADS + tid;
+            wv[k] = j < P ? __ldcg(w + j) : 0.f;
+            pv[k] = j < P ? __ldcg(pos + j) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int j = j0 + k * THREADS + tid;
+            const uint32_t r = evict_rank(wv[k], pv[k], protect);
+            if (held && j < P) ranks[j] = r;
+            count(j < P, r >> 21);
+        }
+    }
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+        if (pass > 0) {
 #pragma unroll 4
-        for (int j = tid; j < P; j += THREADS) {
-            uint32_t r;
-            if (shift == 24) {
-                r = evict_rank(__ldcg(w + j), __ldcg(pos + j), protect);
-                if (held) ranks[j] = r;
-            } else {
-                r = rank_of(j);
+            for (int j = tid; j < (P + 31) / 32 * 32; j += THREADS) {
+                const uint32_t r = j < P ? rank_of(j) : 0u;
+                count(j < P && (r >> (shift + bits)) == prefix, (r >> shift) & ((1u << bits) - 1u));
             }
-            if (shift == 24 || (r >> (shift + 8)) == prefix) atomicAdd(&hist[(r >> shift) & 255u], 1u);
         }
         __syncthreads();
-        if (wid == 0) {
-            // lane l: bins 255 - 8 l down to 248 - 8 l; the bin where the count from above reaches need
-            unsigned int mine[8], sum = 0;
+        // bins from the largest down, BINS of them per thread: the one where the count from above reaches need
+        constexpr int BINS = 2048 / THREADS;
+        unsigned int mine[BINS], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += mine[i] = hist[255 - 8 * lane - i];
-            unsigned int inc = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            unsigned int above = inc - sum;
-            // need = 0 (keep = 0): no bin qualifies, the largest one is taken and nothing of it stays
-            const unsigned int reach = __ballot_sync(0xffffffffu, inc >= need);
-            if (lane == __ffs(reach) - 1) {
-                int i = 0;
-                while (i < 7 && above + mine[i] < need) above += mine[i++];
-                s_pick[0] = (prefix << 8) | static_cast<unsigned int>(255 - 8 * lane - i);
-                s_pick[1] = need - above;
-                s_pick[2] = mine[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) hist[255 - 8 * lane - i] = 0;
+        for (int i = 0; i < BINS; ++i) {
+            sum += mine[i] = hist[2047 - BINS * tid - i];
+            hist[2047 - BINS * tid - i] = 0;
+        }
+        int2 all;
+        unsigned int above = block_exclusive_scan<THREADS>(static_cast<int>(sum), 0, wsum, &all).x;
+        // need = 0 (keep = 0): the first thread takes its first bin, and nothing of it stays
+        if (need == 0 ? tid == 0 : (above < need && need <= above + sum)) {
+            int i = 0;
+            while (i < BINS - 1 && above + mine[i] < need) above += mine[i++];
+            s_pick[0] = (prefix << bits) | ((2047u - BINS * tid - i) & ((1u << bits) - 1u));
+            s_pick[1] = need == 0 ? 0 : need - above;
+            s_pick[2] = mine[i];
         }
         __syncthreads();
         prefix = s_pick[0];
@@ -236,11 +257,9 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
 }
 
 // blockIdx.y: (entry, kv head).  A warp takes eight moves at a time: lane l looks up where row l comes from and goes
-// to, then all of its rows are loaded before the first is stored.  VPR: 16-byte vectors per row; K and V of one row
-// (two, four at smaller head dims) are a warp's 32 vectors.
+// to.  VPR: 16-byte vectors per row.
 template <int VPR>
 __global__ void __launch_bounds__(256) kv_evict_move_kernel(const __grid_constant__ EvictParams p) {
-    constexpr int RPS = 16 / VPR, STEPS = 8 / RPS;  // rows per step, steps per eight moves
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int unit = blockIdx.y, Hkv = p.pages.kv_heads, lane = threadIdx.x & 31;
@@ -249,26 +268,14 @@ __global__ void __launch_bounds__(256) kv_evict_move_kernel(const __grid_constan
     const int* hole_list = ws + 4;
     const int* mover_list = hole_list + p.list_rows;
     const int moves = __ldcg(ws);
-    const int which = (lane / VPR) & 1, vec = lane % VPR, sub = lane / (2 * VPR);
-    uint4* pool = p.pool[which];
+    const uint4* const src[2] = {p.pool[0], p.pool[1]};
     for (int m0 = (blockIdx.x * 8 + threadIdx.x / 32) * 8; m0 < moves; m0 += gridDim.x * 64) {
         long long from = -1, to = -1;
         if (lane < 8 && m0 + lane < moves) {
             from = p.pages.pool_row(b, h, __ldcg(mover_list + m0 + lane));
             to = p.pages.pool_row(b, h, __ldcg(hole_list + m0 + lane));
         }
-        uint4 x[STEPS];
-        long long d[STEPS];
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-            const long long s = __shfl_sync(0xffffffffu, from, k * RPS + sub);
-            d[k] = __shfl_sync(0xffffffffu, to, k * RPS + sub);
-            if (s < 0) d[k] = -1;
-            if (d[k] >= 0) x[k] = __ldcg(pool + s * VPR + vec);
-        }
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k)
-            if (d[k] >= 0) pool[d[k] * VPR + vec] = x[k];
+        copy_rows8<VPR>(src, p.pool, from, to);
     }
     // the lengths come last: P_out may be P_dev, which the first launch read
     if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0) p.P_out[b] = __ldcg(ws + 1);

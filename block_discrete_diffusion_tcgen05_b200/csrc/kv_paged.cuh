@@ -102,6 +102,29 @@ __device__ __forceinline__ int stream_entry(const long long* pre, int batch, lon
     return lo;
 }
 
+// Copies rows of K and V, eight at a time, by one warp: lane l < 8 gives the rows (of VPR 16-byte vectors) that move
+// l reads and writes, -1 for none.  K and V of one row (of two, four at smaller head dims) are the warp's 32 vectors;
+// all of the eight are loaded before the first is stored.
+template <int VPR>
+__device__ __forceinline__ void copy_rows8(const uint4* const (&src)[2], uint4* const (&dst)[2], long long from, long long to) {
+    constexpr int RPS = 16 / VPR, STEPS = 8 / RPS;  // rows per step, steps
+    const int lane = threadIdx.x & 31, which = (lane / VPR) & 1, vec = lane % VPR, sub = lane / (2 * VPR);
+    const uint4* s_base = which ? src[1] : src[0];
+    uint4* d_base = which ? dst[1] : dst[0];
+    if (from < 0) to = -1;
+    uint4 x[STEPS];
+    uint4* d[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        const long long s = __shfl_sync(0xffffffffu, from, k * RPS + sub), t = __shfl_sync(0xffffffffu, to, k * RPS + sub);
+        d[k] = t < 0 ? nullptr : d_base + t * VPR + vec;
+        if (t >= 0) x[k] = __ldcg(s_base + s * VPR + vec);
+    }
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+        if (d[k] != nullptr) *d[k] = x[k];
+}
+
 struct PagedAppendParams {
     PageView pages;
     uint4* pool[2];       // K, V pools
@@ -110,35 +133,33 @@ struct PagedAppendParams {
     float* weight;        // [B][Hkv][capacity] or null: the new rows' accumulated weight becomes 0,
     int* pos;             // [B][Hkv][capacity] or null: their position tokens[b] + i
     const int* tokens;
-    int batch, S_new, vec_per_row;
+    int batch, S_new;
 };
 
-// A pure copy, HBM-bound: 16 bytes per thread-step, grid-stride over the rows of K (blockIdx.y == 0) and V
-// (blockIdx.y == 1); the first thread of a K row also writes its weight and position.
+// A pure copy, HBM-bound: a warp per eight new rows, grid-stride.
+template <int VPR>
 __global__ void __launch_bounds__(256) kv_append_paged_kernel(const __grid_constant__ PagedAppendParams a) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();  // the previous kernel may still read the pool or write the new rows
-    const int which = blockIdx.y;
-    uint4* __restrict__ dst = a.pool[which];
-    const uint4* __restrict__ src = a.src[which];
-    const int Hkv = a.pages.kv_heads, cap = a.pages.capacity();
-    const long long total = static_cast<long long>(a.batch) * Hkv * a.S_new * a.vec_per_row;
-    for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < total;
-         i += static_cast<long long>(gridDim.x) * blockDim.x) {
-        const long long srow = i / a.vec_per_row;
-        const int vec = static_cast<int>(i - srow * a.vec_per_row);
-        const long long unit = srow / a.S_new;
-        const int s = static_cast<int>(srow - unit * a.S_new);
-        const int b = static_cast<int>(unit / Hkv), h = static_cast<int>(unit - static_cast<long long>(b) * Hkv);
-        const long long r = static_cast<long long>(ragged_clamp(__ldcg(a.P_dev + b), cap)) + s;
-        if (r >= cap) continue;  // rows past the capacity are not written
-        if (which == 0 && vec == 0 && a.weight != nullptr) {
-            const long long w = unit * cap + r;
-            a.weight[w] = 0.f;
-            a.pos[w] = __ldcg(a.tokens + b) + s;
+    const int Hkv = a.pages.kv_heads, cap = a.pages.capacity(), lane = threadIdx.x & 31;
+    const long long total = static_cast<long long>(a.batch) * Hkv * a.S_new;
+    for (long long r0 = (blockIdx.x * 8ll + threadIdx.x / 32) * 8; r0 < total; r0 += gridDim.x * 64ll) {
+        const long long from = r0 + lane;
+        long long to = -1;
+        if (lane < 8 && from < total) {
+            const int unit = static_cast<int>(from / a.S_new), s = static_cast<int>(from - static_cast<long long>(unit) * a.S_new);
+            const int b = unit / Hkv, h = unit - b * Hkv;
+            const long long r = static_cast<long long>(ragged_clamp(__ldcg(a.P_dev + b), cap)) + s;
+            if (r < cap) {  // rows past the capacity are not written
+                if (a.weight != nullptr) {
+                    const long long w = static_cast<long long>(unit) * cap + r;
+                    a.weight[w] = 0.f;
+                    a.pos[w] = __ldcg(a.tokens + b) + s;
+                }
+                to = a.pages.pool_row(b, h, static_cast<int>(r));
+            }
         }
-        const long long d = a.pages.pool_row(b, h, static_cast<int>(r));
-        if (d >= 0) dst[d * a.vec_per_row + vec] = __ldcg(src + i);
+        copy_rows8<VPR>(a.src, a.pool, from, to);
     }
 }
 
