@@ -1054,7 +1054,7 @@ PagedLayout paged_layout(const e2d2_dims& dims, int S) {
 static_assert(kPagedMaxCtas * sizeof(int) <= 2048, "tickets");
 
 template <int THREADS>
-e2d2_status launch_evict_select(const EvictParams& a, unsigned units, cudaStream_t stream) {
+e2d2_status launch_evict_select(const EvictParams& a, unsigned units, unsigned cluster, cudaStream_t stream) {
     auto kern = kv_evict_select_kernel<THREADS>;
     static thread_local int configured_dev = -1;
     int dev = 0;
@@ -1064,9 +1064,20 @@ e2d2_status launch_evict_select(const EvictParams& a, unsigned units, cudaStream
             return E2D2_ERR_CUDA;
         configured_dev = dev;
     }
-    return launch_pdl(kern, dim3(units), dim3(THREADS), static_cast<size_t>(a.rank_rows) * 4, stream, a) == cudaSuccess
-               ? E2D2_OK
-               : E2D2_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units * cluster);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.rank_rows) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
 }
 
 // Rows that one list of an eviction can hold, rounded to whole 16 bytes.
@@ -1283,8 +1294,12 @@ e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, 
     a.ws_stride = 4 + 2ll * a.list_rows;
     const unsigned units = static_cast<unsigned>(dims.batch) * dims.kv_heads;
     const long long cap = row_capacity(pages);
-    a.rank_rows = static_cast<int>(cap < kEvictRows ? cap : kEvictRows);
-    s = cap <= 4096 ? launch_evict_select<256>(a, units, stream) : launch_evict_select<1024>(a, units, stream);
+    // blocks per (entry, kv head): as many as leave each 2048 rows and all of them a place on the GPU at once
+    unsigned cluster = 1;
+    while (cluster < 8 && units * cluster * 2 <= static_cast<unsigned>(di->sms) && cap / (cluster * 2) >= 2048) cluster *= 2;
+    const long long slice = ((cap + cluster - 1) / cluster + 31) / 32 * 32;
+    a.rank_rows = static_cast<int>(slice < kEvictRows ? slice : kEvictRows);
+    s = slice <= 4096 ? launch_evict_select<512>(a, units, cluster, stream) : launch_evict_select<1024>(a, units, cluster, stream);
     if (s != E2D2_OK) return s;
     // eight moves per warp and round, at most eight blocks per SM
     const long long most = (a.list_rows + 63) / 64;

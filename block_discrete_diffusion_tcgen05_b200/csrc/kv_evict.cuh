@@ -7,20 +7,24 @@
 // overlap.  Attention over the prefix does not depend on the order of its rows; pos says which token each
 // one is.
 //
-// Two launches: select (one block per (entry, kv head)) finds the kept rows and writes the lists of movers
-// and holes, move copies the K and V rows over the whole GPU.  Select reads 8 bytes a row once, keeps the rows'
-// ranks in shared memory (up to 32768 rows), finds the keep-th largest by 11, 11 and 10 bits in turn (histograms
-// in shared memory; eleven bits tell weights apart that share an exponent, so few lanes meet in a bin) and turns "stays" into one bit a row, from whose counts every row's place in its list follows: no
-// sort, and no atomics but the histograms' counts.
+// Two launches: select finds the kept rows and writes the lists of movers and holes, move copies the K and V rows
+// over the whole GPU.  Select takes a cluster of 1 to 8 blocks per (entry, kv head), each with a slice of the rows.
+// It reads 8 bytes a row once, keeps the slice's ranks in shared memory (up to 32768 rows), and finds the keep-th
+// largest by 11, 11 and 10 bits in turn, from histograms that the blocks read from each other (distributed shared
+// memory); eleven bits tell weights apart that share an exponent, so few lanes meet in a bin, and a pass whose bin
+// stays whole is the last.  Then every warp counts the holes and movers of its rows, and their places in the lists
+// follow from the counts ahead of it: no sort, and no order that depends on timing.
 #pragma once
 
 #include <cstdint>
+
+#include <cooperative_groups.h>
 
 #include "kv_paged.cuh"
 
 namespace e2d2 {
 
-constexpr int kEvictRows = 32768;  // rows whose ranks (and bits) are held in shared memory at a time
+constexpr int kEvictRows = 32768;  // rows whose ranks a block can hold in shared memory
 
 struct EvictParams {
     PageView pages;
@@ -48,125 +52,131 @@ __device__ __forceinline__ uint32_t evict_rank(float w, int pos, int protect_fro
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of (x, y) over the block's threads, their totals in *tx, *ty.  Every thread calls it.
-template <int THREADS>
-__device__ __forceinline__ int2 block_exclusive_scan(int x, int y, int2* wsum, int2* total) {
+// Exclusive prefix of x over the block's warps (x: the same in all lanes of a warp), *total their sum.
+template <int WARPS>
+__device__ __forceinline__ int warps_exclusive(int x, int* wsum, int* total) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int ix = x, iy = y;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, ix, o), b = __shfl_up_sync(0xffffffffu, iy, o);
-        if (lane >= o) ix += a, iy += b;
-    }
-    __syncthreads();  // the previous scan's sums have been read
-    if (lane == 31) wsum[wid] = make_int2(ix, iy);
+    __syncthreads();  // the previous call's sums have been read
+    if (lane == 0) wsum[wid] = x;
     __syncthreads();
-    int2 before = make_int2(ix - x, iy - y), all = make_int2(0, 0);
-#pragma unroll 8
-    for (int i = 0; i < THREADS / 32; ++i) {
-        const int2 s = wsum[i];
-        if (i < wid) before.x += s.x, before.y += s.y;
-        all.x += s.x, all.y += s.y;
-    }
-    *total = all;
-    return before;
+    const int mine = lane < WARPS ? wsum[lane] : 0;
+    *total = __reduce_add_sync(0xffffffffu, mine);
+    return __reduce_add_sync(0xffffffffu, lane < wid ? mine : 0);
 }
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_constant__ EvictParams p) {
-    constexpr int WARPS = THREADS / 32;
-    __shared__ unsigned int hist[2048];
-    __shared__ int2 wsum[WARPS];
-    __shared__ unsigned int s_pick[3];                // leading bits, rows of them that stay, rows that have them
-    __shared__ uint32_t kept_bits[kEvictRows / 32];
-    __shared__ int2 word_at[kEvictRows / 32];         // holes and movers before each 32 rows
-    extern __shared__ uint32_t ranks[];               // [rank_rows]
+    namespace cg = cooperative_groups;
+    constexpr int WARPS = THREADS / 32, BINS = 2048 / THREADS, BATCH = 8;
+    __shared__ __align__(16) unsigned int hist[2][2048];
+    __shared__ int wsum[WARPS];
+    __shared__ unsigned int s_pick[3];  // leading bits, rows of them that stay, rows that have them
+    __shared__ int s_count[3];          // this block's rows at the threshold, holes, movers
+    extern __shared__ uint32_t ranks[]; // [rank_rows]
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
     ptx::griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    for (int i = tid; i < 2 * 2048; i += THREADS) (&hist[0][0])[i] = 0;
     ptx::griddep_wait();
-    const int unit = blockIdx.x, Hkv = p.pages.kv_heads, cap = p.pages.capacity();
-    const int b = unit / Hkv, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int unit = blockIdx.x / blocks, Hkv = p.pages.kv_heads, cap = p.pages.capacity();
+    const int b = unit / Hkv;
     const int P = ragged_clamp(__ldcg(p.P_dev + b), cap);
+    // the first protected position, without overflow for any recent >= 0
+    const long long pf = static_cast<long long>(__ldcg(p.tokens + b)) - p.recent;
+    const int protect = pf < INT_MIN ? INT_MIN : static_cast<int>(pf);
     const long long row0 = static_cast<long long>(unit) * cap;
     const float* w = p.weight + row0;
     const int* pos = p.pos + row0;
     float* w_out = p.weight_out + row0;
     int* pos_out = p.pos_out + row0;
     int* ws = p.ws + unit * p.ws_stride;
-    if (P <= p.keep) {
-        if (tid == 0) {
-            ws[0] = 0;
-            ws[1] = P;
-        }
-        if (w_out != w || pos_out != pos)
-            for (int j = tid; j < P; j += THREADS) {
-                w_out[j] = w[j];
-                pos_out[j] = pos[j];
+    const bool copy = w_out != w || pos_out != pos;
+    const int per = ((P + blocks - 1) / blocks + 31) / 32 * 32;  // rows of a block
+    const int beg = min(me * per, P), rows = min(beg + per, P) - beg;
+    const int kept = min(P, p.keep);
+    if (P <= p.keep) {  // the same for every block of the cluster
+        if (copy)
+            for (int j = beg + tid; j < beg + rows; j += THREADS) {
+                w_out[j] = __ldcg(w + j);
+                pos_out[j] = __ldcg(pos + j);
             }
+        if (me == 0 && tid == 0) {
+            ws[0] = 0;
+            ws[1] = kept;
+        }
         return;
     }
-    // the first protected position, without overflow for any recent >= 0
-    const long long pf = static_cast<long long>(__ldcg(p.tokens + b)) - p.recent;
-    const int protect = pf < INT_MIN ? INT_MIN : static_cast<int>(pf);
-    const bool held = P <= p.rank_rows;
-    auto rank_of = [&](int j) { return held ? ranks[j] : evict_rank(__ldcg(w + j), __ldcg(pos + j), protect); };
-    for (int i = tid; i < 2048; i += THREADS) hist[i] = 0;
+    const bool held = rows <= p.rank_rows;
+    auto rank_of = [&](int i) { return held ? ranks[i] : evict_rank(__ldcg(w + beg + i), __ldcg(pos + beg + i), protect); };
     __syncthreads();
 
-    // The keep-th largest rank, 11, 11 and 10 bits a pass: prefix = its leading bits, need = how many rows with that
-    // prefix stay.  The first pass also fills the ranks.
-    unsigned int prefix = 0, need = p.keep, equal = 0;
-    auto count = [&](bool in, uint32_t bin) {
-        // equal weights (a fresh cache's zeros) would queue at one bin: a warp of one bin counts once
-        const unsigned int lanes = __ballot_sync(0xffffffffu, in);
-        if (lanes == 0) return;
-        const int lead = __ffs(lanes) - 1;
-        const uint32_t first = __shfl_sync(0xffffffffu, bin, lead);
-        if (__all_sync(0xffffffffu, !in || bin == first)) {
-            if (lane == lead) atomicAdd(&hist[bin], __popc(lanes));
-        } else if (in) {
-            atomicAdd(&hist[bin], 1u);
-        }
-    };
-    constexpr int BATCH = 8;
+    // One read of the rows: their ranks, the first histogram, and (unless in place) the copy of the rows below keep;
+    // the movers overwrite the holes among them at the end.
 #pragma unroll 1
-    for (int j0 = 0; j0 < P; j0 += BATCH * THREADS) {
+    for (int i0 = tid; i0 < rows; i0 += BATCH * THREADS) {
         float wv[BATCH];
         int pv[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int j = j0 + k * THREADS + tid;
-            wv[k] = j < P ? __ldcg(w + j) : 0.f;
-            pv[k] = j < P ? __ldcg(pos + j) : 0;
+            const int i = i0 + k * THREADS;
+            if (i < rows) wv[k] = __ldcg(w + beg + i), pv[k] = __ldcg(pos + beg + i);
         }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int j = j0 + k * THREADS + tid;
+            const int i = i0 + k * THREADS;
+            if (i >= rows) break;
             const uint32_t r = evict_rank(wv[k], pv[k], protect);
-            if (held && j < P) ranks[j] = r;
-            count(j < P, r >> 21);
+            if (held) ranks[i] = r;
+            atomicAdd(&hist[0][r >> 21], 1u);
+            if (copy && beg + i < p.keep) w_out[beg + i] = wv[k], pos_out[beg + i] = pv[k];
         }
     }
+    // The keep-th largest rank, 11, 11 and 10 bits a pass: prefix = its leading bits, need = how many rows with that
+    // prefix stay; done when all of them do.
+    unsigned int prefix = 0, need = p.keep, equal = 0;
+    int shift = 21, bits = 11;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+    for (int pass = 0;; ++pass) {
         if (pass > 0) {
+            const unsigned int mask = (1u << bits) - 1u;
 #pragma unroll 4
-            for (int j = tid; j < (P + 31) / 32 * 32; j += THREADS) {
-                const uint32_t r = j < P ? rank_of(j) : 0u;
-                count(j < P && (r >> (shift + bits)) == prefix, (r >> shift) & ((1u << bits) - 1u));
+            for (int i = tid; i < rows; i += THREADS) {
+                const uint32_t r = rank_of(i);
+                if ((r >> (shift + bits)) == prefix) atomicAdd(&hist[pass & 1][(r >> shift) & mask], 1u);
             }
         }
-        __syncthreads();
+        cluster.sync();
         // bins from the largest down, BINS of them per thread: the one where the count from above reaches need
-        constexpr int BINS = 2048 / THREADS;
         unsigned int mine[BINS], sum = 0;
 #pragma unroll
-        for (int i = 0; i < BINS; ++i) {
-            sum += mine[i] = hist[2047 - BINS * tid - i];
-            hist[2047 - BINS * tid - i] = 0;
+        for (int i = 0; i < BINS; ++i) mine[i] = 0;
+        for (int c = 0; c < blocks; ++c) {
+            const unsigned int* h = cluster.map_shared_rank(&hist[pass & 1][0], c) + 2048 - BINS * (tid + 1);
+            if constexpr (BINS % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < BINS; i += 4) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(h + BINS - 4 - i);
+                    mine[i] += x.w, mine[i + 1] += x.z, mine[i + 2] += x.y, mine[i + 3] += x.x;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < BINS; ++i) mine[i] += h[BINS - 1 - i];
+            }
         }
-        int2 all;
-        unsigned int above = block_exclusive_scan<THREADS>(static_cast<int>(sum), 0, wsum, &all).x;
+#pragma unroll
+        for (int i = 0; i < BINS; ++i) sum += mine[i];
+        unsigned int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        int all;
+        unsigned int above = warps_exclusive<WARPS>(static_cast<int>(__shfl_sync(0xffffffffu, inc, 31)), wsum, &all) + inc - sum;
+        // every block has read the other histogram (the cluster has met since): it is clear for the pass after next
+        if (pass == 1)
+            for (int i = tid; i < 2048; i += THREADS) hist[0][i] = 0;
         // need = 0 (keep = 0): the first thread takes its first bin, and nothing of it stays
         if (need == 0 ? tid == 0 : (above < need && need <= above + sum)) {
             int i = 0;
@@ -179,80 +189,80 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
         prefix = s_pick[0];
         need = s_pick[1];
         equal = s_pick[2];
+        if (need == equal || shift == 0) break;
+        bits = pass == 0 ? 11 : 10;
+        shift -= bits;
     }
-    // Rows above the threshold stay, and the first `need` of the rows that equal it.
+    // Rows above the threshold stay, and the first `need` of the `equal` rows at it.  A warp takes a run of the
+    // block's rows, 32 at a time, in their order.
     int* hole_list = ws + 4;
     int* mover_list = hole_list + p.list_rows;
-    int eq_seen = 0;
-    int2 seen = make_int2(0, 0);  // holes, movers
-    const bool copy = w_out != w || pos_out != pos;
-#pragma unroll 1
-    for (int base = 0; base < P; base += kEvictRows) {
-        const int rows = min(P - base, kEvictRows), words = (rows + 31) / 32;
-        const int per = (words + WARPS - 1) / WARPS, w0 = min(wid * per, words), w1 = min(w0 + per, words);
-        int eq_before = 0;
-        if (equal != need) {  // ties at the threshold: which of them are the first
-            int mine = 0;
-            for (int k = w0; k < w1; ++k) {
-                const int j = base + 32 * k + lane;
-                mine += __popc(__ballot_sync(0xffffffffu, j < P && rank_of(j) == prefix));
-            }
-            int2 all;
-            eq_before = eq_seen + block_exclusive_scan<THREADS>(lane == 0 ? mine : 0, 0, wsum, &all).x;
-            eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
-            eq_seen += all.x;
-        }
-        __syncthreads();  // the last round's bits have been read
-#pragma unroll 2
-        for (int k = w0; k < w1; ++k) {
-            const int j = base + 32 * k + lane;
-            const uint32_t r = j < P ? rank_of(j) : 0u;
-            const bool eq = j < P && r == prefix;
-            const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-            const bool stay = (j < P && r > prefix) ||
-                              (eq && (equal == need || eq_before + __popc(eqs & ((1u << lane) - 1u)) < static_cast<int>(need)));
-            eq_before += __popc(eqs);
-            const uint32_t bits = __ballot_sync(0xffffffffu, stay);
-            if (lane == 0) kept_bits[k] = bits;
-        }
-        __syncthreads();
-        for (int k0 = 0; k0 < words; k0 += THREADS) {
-            const int k = k0 + tid, j = base + 32 * k;
-            int2 n = make_int2(0, 0), all;
-            if (k < words) {
-                // rows of the word below keep, a mask
-                const uint32_t low = j + 32 <= p.keep ? 0xffffffffu : (j >= p.keep ? 0u : (1u << (p.keep - j)) - 1u);
-                n = make_int2(__popc(~kept_bits[k] & low), __popc(kept_bits[k] & ~low));
-            }
-            const int2 at = block_exclusive_scan<THREADS>(n.x, n.y, wsum, &all);
-            if (k < words) word_at[k] = make_int2(seen.x + at.x, seen.y + at.y);
-            seen.x += all.x, seen.y += all.y;
-        }
-        __syncthreads();
-#pragma unroll 2
-        for (int k = w0; k < w1; ++k) {
-            const int j = base + 32 * k + lane;
-            const uint32_t bits = kept_bits[k], below = (1u << lane) - 1u;
-            const uint32_t low = j - lane + 32 <= p.keep ? 0xffffffffu : (j - lane >= p.keep ? 0u : (1u << (p.keep - (j - lane))) - 1u);
-            const int2 at = word_at[k];
-            const bool stay = (bits >> lane) & 1u;
-            if (j < p.keep && !stay) hole_list[at.x + __popc(~bits & low & below)] = j;
-            if (j >= p.keep && stay) mover_list[at.y + __popc(bits & ~low & below)] = j;
-            if (copy && j < p.keep && stay) {
-                w_out[j] = __ldcg(w + j);
-                pos_out[j] = __ldcg(pos + j);
-            }
-        }
+    const int run = ((rows + WARPS - 1) / WARPS + 31) / 32 * 32;
+    const int i_beg = min(wid * run, rows), i_end = min(i_beg + run, rows);
+    const bool ties = need != equal;
+    int eq_before = 0;  // rows at the threshold ahead of this warp's
+    if (ties) {
+        int n = 0, all;
+        for (int i = i_beg; i < i_end; i += 32)
+            n += __popc(__ballot_sync(0xffffffffu, i + lane < rows && (rank_of(min(i + lane, rows - 1)) >> shift) == prefix));
+        eq_before = warps_exclusive<WARPS>(n, wsum, &all);
+        if (tid == 0) s_count[0] = all;
+        cluster.sync();
+        for (int c = 0; c < me; ++c) eq_before += *cluster.map_shared_rank(&s_count[0], c);
     }
-    __syncthreads();  // the lists are written; movers and holes are equally many
-    for (int i = tid; i < seen.y; i += THREADS) {
-        const int s = mover_list[i], d = hole_list[i];
-        w_out[d] = w[s];
-        pos_out[d] = pos[s];
+    // whether row i stays; `eqs` counts the rows at the threshold on the way
+    auto stays = [&](int i, int& eqs) {
+        const uint32_t r = (i < rows ? rank_of(i) : 0u) >> shift;
+        const bool eq = i < rows && r == prefix;
+        bool stay = i < rows && r >= prefix;
+        if (ties) {
+            const uint32_t m = __ballot_sync(0xffffffffu, eq);
+            if (eq) stay = eqs + __popc(m & ((1u << lane) - 1u)) < static_cast<int>(need);
+            eqs += __popc(m);
+        }
+        return stay;
+    };
+    int holes = 0, movers = 0, eqs = eq_before;
+#pragma unroll 4
+    for (int i = i_beg; i < i_end; i += 32) {
+        const bool stay = stays(i + lane, eqs), in = i + lane < rows, low = beg + i + lane < p.keep;
+        holes += __popc(__ballot_sync(0xffffffffu, in && low && !stay));
+        movers += __popc(__ballot_sync(0xffffffffu, in && !low && stay));
     }
+    int all_holes, all_movers;
+    holes = warps_exclusive<WARPS>(holes, wsum, &all_holes);
+    movers = warps_exclusive<WARPS>(movers, wsum, &all_movers);
     if (tid == 0) {
-        ws[0] = seen.y;
-        ws[1] = p.keep;
+        s_count[1] = all_holes;
+        s_count[2] = all_movers;
+    }
+    cluster.sync();
+    int moves = 0;
+    for (int c = 0; c < blocks; ++c) {
+        const int* n = cluster.map_shared_rank(&s_count[0], c);
+        if (c < me) holes += n[1], movers += n[2];
+        moves += n[2];
+    }
+    eqs = eq_before;
+#pragma unroll 4
+    for (int i = i_beg; i < i_end; i += 32) {
+        const int j = beg + i + lane;
+        const bool stay = stays(i + lane, eqs), in = i + lane < rows, low = j < p.keep;
+        const uint32_t h = __ballot_sync(0xffffffffu, in && low && !stay), m = __ballot_sync(0xffffffffu, in && !low && stay);
+        const uint32_t ahead = (1u << lane) - 1u;
+        if (in && low && !stay) hole_list[holes + __popc(h & ahead)] = j;
+        if (in && !low && stay) mover_list[movers + __popc(m & ahead)] = j;
+        holes += __popc(h), movers += __popc(m);
+    }
+    cluster.sync();  // the lists are written; movers and holes are equally many
+    for (int i = me * THREADS + tid; i < moves; i += blocks * THREADS) {
+        const int s = __ldcg(mover_list + i), d = __ldcg(hole_list + i);
+        w_out[d] = __ldcg(w + s);
+        pos_out[d] = __ldcg(pos + s);
+    }
+    if (me == 0 && tid == 0) {
+        ws[0] = moves;
+        ws[1] = kept;
     }
 }
 
