@@ -13,7 +13,7 @@ import torch
 
 from . import _lib
 
-_BF16 = torch.bfloat16
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _dims(batch, q_heads, kv_heads, head_dim, scale):
@@ -21,6 +21,8 @@ def _dims(batch, q_heads, kv_heads, head_dim, scale):
 
 
 def _need(t: torch.Tensor, name: str, dtype=_BF16, ndim=4):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -37,15 +39,20 @@ def _device_guard(fn):
     """Runs a call with the GPU of its first tensor current (the C calls read the current device:
     SM count, error word) and rejects tensors spread over several devices."""
 
+    Tensor = torch.Tensor
+
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         first = args[0] if args else None
-        if isinstance(first, torch.Tensor) and first.is_cuda:
+        if isinstance(first, Tensor) and first.is_cuda:
             idx = first.get_device()
-            for a in (*args, *kwargs.values()):
-                if isinstance(a, torch.Tensor) and a.get_device() != idx:
+            for a in args:
+                if isinstance(a, Tensor) and a.get_device() != idx:
                     raise ValueError(f"{fn.__name__}: every tensor must be on cuda:{idx}")
-            if idx != torch.cuda.current_device():
+            for a in kwargs.values():
+                if isinstance(a, Tensor) and a.get_device() != idx:
+                    raise ValueError(f"{fn.__name__}: every tensor must be on cuda:{idx}")
+            if idx != torch._C._cuda_getDevice():
                 with torch.cuda.device(idx):
                     return fn(*args, **kwargs)
         return fn(*args, **kwargs)
@@ -67,7 +74,7 @@ def _out_tensor(out, like: torch.Tensor) -> torch.Tensor:
 def _lse_tensor(lse, shape, device):
     """lse=True: a new fp32 tensor; None/False: not computed; a tensor: the caller's, checked."""
     if lse is True:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return torch.empty(shape, dtype=_F32, device=device)
     if lse is None or lse is False:
         return None
     _need(lse, "lse", dtype=torch.float32, ndim=3)
@@ -87,7 +94,9 @@ def _ptr(t):
 
 
 def _stream(t: torch.Tensor):
-    return ctypes_stream(torch.cuda.current_stream(t.device))
+    """The handle of the current stream of t's device (what torch.cuda.current_stream(t.device) wraps, without
+    building the wrapper for every call)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def ctypes_stream(s: torch.cuda.Stream):
@@ -377,7 +386,7 @@ def _pages(k_pages: torch.Tensor, page_table, batch: int):
         if num_pages != batch:
             raise ValueError("without a page table the caches must be [B, Hkv, capacity, d]")
         return _lib.Pages(num_pages, page_rows, 1, None), page_rows
-    _need(page_table, "page_table", dtype=torch.int32, ndim=2)
+    _need(page_table, "page_table", dtype=_I32, ndim=2)
     if page_table.shape[0] != batch:
         raise ValueError("page_table must be [B, max_pages]")
     max_pages = page_table.shape[1]
@@ -385,13 +394,13 @@ def _pages(k_pages: torch.Tensor, page_table, batch: int):
 
 
 def _need_ints(t, name: str, batch: int):
-    _need(t, name, dtype=torch.int32, ndim=1)
+    _need(t, name, _I32, 1)
     if t.shape[0] != batch:
         raise ValueError(f"{name} must be [B]")
 
 
 def _need_rows(t, name: str, shape, dtype):
-    _need(t, name, dtype=dtype, ndim=3)
+    _need(t, name, dtype, 3)
     if t.shape != shape:
         raise ValueError(f"{name} must be [B, Hkv, row capacity] = {tuple(shape)}, got {tuple(t.shape)}")
 
