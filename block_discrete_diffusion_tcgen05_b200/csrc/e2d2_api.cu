@@ -1213,6 +1213,9 @@ e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages p
     s = check_pages(pages, dims);
     if (s != E2D2_OK) return s;
     if (static_cast<long long>(dims.batch) * dims.q_heads * S > kMaxI32 / 8) return E2D2_ERR_SHAPE;
+    // every tile index of the stream fits in 31 bits
+    if (static_cast<long long>(dims.batch) * dims.kv_heads * (row_capacity(pages) / kWeighKeys + 1) > kMaxI32)
+        return E2D2_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned4(P_dev) || !aligned4(lse) || !aligned4(weight) ||
         !aligned4(weight_out))
         return E2D2_ERR_ALIGNMENT;

@@ -61,45 +61,63 @@ __device__ __forceinline__ bool wait_stage_warp(uint64_t* bar, uint32_t parity, 
     return wait_bar_warp(bar, parity, abort_flag, err);
 }
 
-// The work of a call as one stream: entry b takes count(b) items.  Fills pre[0..batch-1] with the items before
-// each entry (shared memory, as is sums[THREADS / 32]) and returns the sum of all.  Every thread of a block of
-// THREADS calls it; pre is readable after it.
-template <int THREADS, class Count>
-__device__ __forceinline__ long long stream_prefix(int batch, long long* pre, long long* sums, Count count) {
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int per = (batch + THREADS - 1) / THREADS, b0 = tid * per;
-    long long mine = 0;
-    for (int i = b0; i < b0 + per && i < batch; ++i) mine += count(i);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    long long before = inc - mine, total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        before += w < warp ? sums[w] : 0;
-        total += sums[w];
-    }
-    for (int i = b0; i < b0 + per && i < batch; ++i) {
-        pre[i] = before;
-        before += count(i);
-    }
-    __syncthreads();
-    return total;
-}
+// The work of a call as one stream of places: entry b takes units * places(P[b]) of them, the entries one after the
+// other (below 2^31 in all, the host sees to it).  Every warp works it out for itself, a lane per entry, 32 entries
+// at a time: no shared memory, no barrier.
+template <class Places>
+struct EntryStream {
+    const int* P_dev;
+    int batch, cap, lane;
+    unsigned units, lead;  // lead: places of every unit on top of places(P)
+    Places places;
+    int P;                // of lane's entry in the batch of 32 at hand
+    unsigned n;
+    unsigned total;       // places in all
+    bool equal;           // every entry takes as many
 
-// The entry that holds item pos of the stream: pre[b] <= pos.
-__device__ __forceinline__ int stream_entry(const long long* pre, int batch, long long pos) {
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= pos) lo = mid;
-        else hi = mid;
+    __device__ EntryStream(const int* lengths, int b, int capacity, unsigned units_per_entry, Places f)
+        : P_dev(lengths), batch(b), cap(capacity), lane(threadIdx.x & 31), units(units_per_entry), lead(0), places(f) {
+        unsigned sum = 0, most = 0;
+        for (int base = 0; base < batch; base += 32) {
+            load(base);
+            sum += __reduce_add_sync(0xffffffffu, n);
+            most = max(most, __reduce_max_sync(0xffffffffu, n));
+        }
+        total = sum * units;
+        equal = sum == most * batch;
     }
-    return lo;
+    __device__ void load(int base) {
+        P = base + lane < batch ? ragged_clamp(__ldcg(P_dev + base + lane), cap) : 0;
+        n = base + lane < batch ? places(P) : 0;
+    }
+    // The entry that holds place pos < total, the places before it and its length.
+    __device__ void find(unsigned pos, int& entry, unsigned& before, int& length) {
+        before = 0;
+        for (int base = 0;; base += 32) {
+            if (batch > 32) load(base);
+            const unsigned mine = base + lane < batch ? n + lead : 0;
+            unsigned inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + inc * units > pos);
+            if (past != 0 || base + 32 >= batch) {
+                const int at = past != 0 ? __ffs(past) - 1 : 31;
+                entry = base + at;
+                before += __shfl_sync(0xffffffffu, inc - mine, at) * units;
+                length = __shfl_sync(0xffffffffu, P, at);
+                return;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31) * units;
+        }
+    }
+};
+
+template <class Places>
+__device__ __forceinline__ EntryStream<Places> entry_stream(const int* P_dev, int batch, int cap, unsigned units, Places f) {
+    return EntryStream<Places>(P_dev, batch, cap, units, f);
 }
 
 // Copies rows of K and V, eight at a time, by one warp: lane l < 8 gives the rows (of VPR 16-byte vectors) that move

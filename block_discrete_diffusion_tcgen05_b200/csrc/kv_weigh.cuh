@@ -59,36 +59,37 @@ struct WeighCfg {
     // k_full[NST], k_empty[NST], q_full[QB], q_empty[QB], s_full[2], s_free[2], drain, done
     static constexpr int NBAR = 2 * NST + 2 * QB + 6;
     static constexpr int OFF_LSE = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // float [8 warps][N]
-    static constexpr int OFF_PRE = OFF_LSE + 8 * N * 4;                  // long long [kPagedMaxBatch]
-    static constexpr int OFF_MISC = OFF_PRE + kPagedMaxBatch * 8;        // holder, abort, scan sums
-    static constexpr int BYTES = OFF_MISC + 16 + 8 * (kWeighThreads / 32);
+    static constexpr int OFF_MISC = OFF_LSE + 8 * N * 4;                       // holder, abort
+    static constexpr int BYTES = OFF_MISC + 8;
     static constexpr int ALLOC = (BYTES + 1023) / 1024 * 1024 + 1024;
     static_assert(NST >= 2 && ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
 };
 
-// Walks the tiles of this block: unit (entry b, kv head), key tile t of it.
+__device__ __forceinline__ unsigned weigh_tiles(int P) { return (P + kWeighKeys - 1) / kWeighKeys; }
+
+// Walks the tiles of this block: unit (entry b, kv head h), key tile t of it.
 struct WeighWalk {
     const WeighParams& p;
-    long long left;  // tiles still to come
+    unsigned left;   // tiles still to come
     int b, h, P, tiles;
     int unit, t;     // the current tile's unit (b * Hkv + h) and index
 
-    __device__ WeighWalk(const WeighParams& prm, const long long* pre, long long first, long long last)
-        : p(prm), left(last - first), b(0), h(0), P(0), tiles(0), unit(0), t(0) {
-        if (left <= 0) return;
-        b = stream_entry(pre, p.batch, first);  // holds a tile, so it has rows
-        load();
-        const long long in = first - pre[b];
-        h = static_cast<int>(in / tiles);
-        t = static_cast<int>(in - static_cast<long long>(h) * tiles) - 1;
-    }
-    __device__ void load() {
-        P = ragged_clamp(__ldcg(p.P_dev + b), p.pages.capacity());
-        tiles = (P + kWeighKeys - 1) / kWeighKeys;
+    template <class Stream>
+    __device__ WeighWalk(const WeighParams& prm, Stream stream)
+        : p(prm), b(0), h(0), P(0), tiles(0), unit(0), t(0) {
+        const unsigned q = stream.total / gridDim.x, r = stream.total % gridDim.x, c = blockIdx.x;
+        const unsigned first = c * q + c * r / gridDim.x;
+        left = (c + 1) * q + (c + 1) * r / gridDim.x - first;
+        if (left == 0) return;
+        unsigned before;
+        stream.find(first, b, before, P);
+        tiles = weigh_tiles(P);
+        h = (first - before) / tiles;
+        t = static_cast<int>(first - before - h * tiles) - 1;
     }
     // Moves to the next tile; false at the end.
     __device__ bool next() {
-        if (left <= 0) return false;
+        if (left == 0) return false;
         --left;
         if (++t == tiles) {
             t = 0;
@@ -96,7 +97,8 @@ struct WeighWalk {
                 h = 0;
                 do {
                     ++b;
-                    load();
+                    P = ragged_clamp(__ldcg(p.P_dev + b), p.pages.capacity());
+                    tiles = weigh_tiles(P);
                 } while (tiles == 0);  // a tile is left, so an entry with rows follows
             }
         }
@@ -119,10 +121,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
     uint64_t* s_free = s_full + 2;
     uint64_t* drain = s_free + 2;
     uint64_t* done = drain + 1;
-    long long* pre = reinterpret_cast<long long*>(smem + C::OFF_PRE);
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-    long long* sums = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);
 
     ptx::griddep_launch_dependents();
     if (threadIdx.x == 0) {
@@ -140,14 +140,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
     }
     ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
     const int cap = p.pages.capacity(), Hkv = p.pages.kv_heads;
-    const long long total = stream_prefix<kWeighThreads>(p.batch, pre, sums, [&](int i) {
-        return static_cast<long long>(Hkv) * ((ragged_clamp(__ldcg(p.P_dev + i), cap) + kWeighKeys - 1) / kWeighKeys);
-    });
+    const auto stream = entry_stream(p.P_dev, p.batch, cap, Hkv, [](int rows) { return weigh_tiles(rows); });
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
-    const long long first = range_begin(blockIdx.x, total, gridDim.x), last = range_begin(blockIdx.x + 1, total, gridDim.x);
     const int n16 = round16(p.n);
 
     if (warp == 0) {
@@ -159,7 +156,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         }
         test_producer_delay();
         const int boxes = kWeighKeys / p.box_rows;
-        WeighWalk walk(p, pre, first, last);
+        WeighWalk walk(p, stream);
         int unit = 0, y = -1, z = 0;
         auto look_up = [&]() {
             if (!walk.next()) return false;
@@ -220,7 +217,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         const uint64_t desc = ptx::smem_desc(0, 16, 8 * C::RB, C::SWZ);  // K (A) and Q (B): K-major
         const uint32_t idesc = ptx::idesc_bf16_f32(kWeighKeys, n16, false, false);
         constexpr int KPC = C::RB / 32;  // 16-element steps per column chunk
-        WeighWalk walk(p, pre, first, last);
+        WeighWalk walk(p, stream);
         uint32_t it = 0, units = 0;
         int have = -1;
         bool ok = true;
@@ -262,24 +259,38 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         // Warpgroup g takes every other tile; every warp has its own copy of the normalisers.
         const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane;
         float* lse2 = reinterpret_cast<float*>(smem + C::OFF_LSE) + (warp - 4) * N;
-        WeighWalk walk(p, pre, first, last);
-        uint32_t it = 0;
-        int have = -1;
-        while (walk.next()) {
-            const uint32_t n_it = it++;
-            if (static_cast<int>(n_it & 1) != g) continue;
+        WeighWalk walk(p, stream);
+        // The tile ahead: its weight and whether a page backs it are on their way while this one's scores are waited
+        // for.  at < 0: no row of this thread's.
+        int unit_n = -1;
+        long long at_n = -1;
+        float before_n = 0.f;
+        bool backed_n = false;
+        auto ahead = [&](int skip) {
+            bool more = true;
+            for (int i = 0; i <= skip && more; ++i) more = walk.next();
+            at_n = -1;
+            if (!more) return false;
+            unit_n = walk.unit;
             const int j = walk.t * kWeighKeys + key;
-            const bool live = j < walk.P;
-            const long long at = static_cast<long long>(walk.unit) * cap + j;
-            float sum = 0.f, before = 0.f;
-            bool backed = false;
-            if (live) {
-                before = __ldcg(p.weight + at);
+            if (j < walk.P) {
+                at_n = static_cast<long long>(unit_n) * cap + j;
+                before_n = __ldcg(p.weight + at_n);
                 int in_page;
-                backed = p.pages.locate(walk.b, j, in_page) >= 0;
+                backed_n = p.pages.locate(walk.b, j, in_page) >= 0;
             }
-            if (walk.unit != have) {
-                have = walk.unit;
+            return true;
+        };
+        int have = -1;
+        bool more = ahead(g);
+        for (uint32_t use = 0; more; ++use) {
+            const int unit = unit_n;
+            const long long at = at_n;
+            const float before = before_n;
+            const bool backed = backed_n;
+            more = ahead(1);
+            if (unit != have) {
+                have = unit;
                 __syncwarp();  // the last unit's values have been read
                 for (int c = lane; c < n16; c += 32) {
                     const float x = c < p.n ? __ldcg(p.lse + static_cast<long long>(have) * p.rows + p.row0 + c) : -INFINITY;
@@ -287,17 +298,20 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
                 }
                 __syncwarp();
             }
-            if (!wait_stage_warp(&s_full[g], (n_it >> 1) & 1, abort_flag, p.err)) break;
+            if (!wait_stage_warp(&s_full[g], use & 1, abort_flag, p.err)) break;
             ptx::tc_fence_after();
-            for (int c0 = 0; c0 < n16; c0 += 16) {
-                uint32_t raw[16];
-                ptx::tmem_ld16(tmem + g * N + (static_cast<uint32_t>(32 * w) << 16) + c0, raw);
+            float sum = 0.f;
+            for (int c0 = 0; c0 < n16; c0 += 32) {
+                // columns past the last row hold another unit's query, or none, or (past n16) old scores: they add
+                // nothing whatever they are
+                uint32_t raw[32];
+                const uint32_t ta = tmem + g * N + (static_cast<uint32_t>(32 * w) << 16) + c0;
+                ptx::tmem_ld32(ta, raw);
                 ptx::tmem_wait_ld();
-                ptx::reg_fence<16>(raw);
-                // columns past the last row hold another unit's query, or none: they add nothing whatever it is
+                ptx::reg_fence<32>(raw);
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 32; ++c) {
                     const float e = ptx::ex2(__uint_as_float(raw[c]) * p.scale_log2 - lse2[c0 + c]);
                     part[c & 3] += c0 + c < p.n ? e : 0.f;
                 }
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             }
             ptx::tc_fence_before();
             ptx::mbar_arrive(&s_free[g]);
-            if (live) p.weight_out[at] = before + (backed ? sum : 0.f);
+            if (at >= 0) p.weight_out[at] = before + (backed ? sum : 0.f);
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(done);

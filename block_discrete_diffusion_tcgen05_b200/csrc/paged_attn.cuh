@@ -302,51 +302,24 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     }
     ptx::griddep_wait();  // lengths, table and rows are read after the previous kernel on the stream
 
-    // ---- schedule: this block's range of the stream and the entry it starts in.  Every warp works it out for
-    // itself, a lane per entry, 32 entries at a time.
+    // ---- schedule: this block's range of the stream and the entry it starts in
     const int Hkv = p.pages.kv_heads, cap = p.pages.capacity();
     const int upe = Hkv * p.qtiles;  // units per entry
     const int own_rows = p.own ? p.S : 0;
     const int n_own = (own_rows + KEYS - 1) / KEYS;
-    int P = 0, stages = 0;           // of the entry at hand; first, of lane's entry in a batch of 32
-    auto lane_entry = [&](int base) {
-        P = base + lane < p.batch ? ragged_clamp(__ldcg(p.P_dev + base + lane), cap) : 0;
-        stages = base + lane < p.batch ? max(1, paged_stages(P, own_rows, KEYS)) : 0;
-    };
-    unsigned sum = 0, most = 0;      // stages of one unit of every entry, of the longest
-    for (int base = 0; base < p.batch; base += 32) {
-        lane_entry(base);
-        sum += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(stages));
-        most = max(most, __reduce_max_sync(0xffffffffu, static_cast<unsigned>(stages)));
+    auto stream = entry_stream(p.P_dev, p.batch, cap, upe,
+                               [&](int rows) { return static_cast<unsigned>(max(1, paged_stages(rows, own_rows, KEYS))); });
+    const unsigned lead = stream.equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
+    if (lead > 0) {
+        stream.lead = lead;
+        stream.total += lead * p.batch * upe;
     }
-    const bool equal = sum == most * p.batch;
-    const unsigned lead = equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
-    const unsigned total = (sum + lead * p.batch) * upe;
-    const StreamCut cut(total, paged_parts(total, p.batch * upe, equal, gridDim.x, KEYS));
+    const StreamCut cut(stream.total, paged_parts(stream.total, p.batch * upe, stream.equal, gridDim.x, KEYS));
     if (static_cast<int>(blockIdx.x) >= cut.parts) return;
-    unsigned pos = cut.begin(blockIdx.x);
+    unsigned pos = cut.begin(blockIdx.x), ent_beg;
     const unsigned end = cut.begin(blockIdx.x + 1);
-    int b = 0;
-    unsigned ent_beg = 0;
-    for (int base = 0;; base += 32) {
-        if (p.batch > 32) lane_entry(base);
-        const unsigned places = stages > 0 ? stages + lead : 0;
-        unsigned inc = places;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, ent_beg + inc * upe > pos);
-        if (past != 0 || base + 32 >= p.batch) {
-            const int at = past != 0 ? __ffs(past) - 1 : 31;
-            b = base + at;
-            ent_beg += __shfl_sync(0xffffffffu, inc - places, at) * upe;
-            P = __shfl_sync(0xffffffffu, P, at);
-            break;
-        }
-        ent_beg += __shfl_sync(0xffffffffu, inc, 31) * upe;
-    }
+    int b, P;
+    stream.find(pos, b, ent_beg, P);
     if (loads) test_producer_delay();
     __syncthreads();  // the barriers are initialised
 
