@@ -28,15 +28,19 @@ struct PageView {
 
     __device__ __forceinline__ int capacity() const { return max_pages * page_rows; }
 
-    // Page that holds row r of entry b (r inside the capacity), and the row inside it; -1, with the error recorded,
-    // if the table names no page of the pool.  Nothing is read or written through such an entry.
-    __device__ __forceinline__ int locate(int b, int r, int& in_page) const {
+    // The table's entry for row r of entry b (r inside the capacity), and the row inside the page.  Loaded, not
+    // looked at: what page() makes of it can wait until the load is back.
+    __device__ __forceinline__ int entry(int b, int r, int& in_page) const {
         in_page = r;
         if (table == nullptr) return b;
         const int at = static_cast<unsigned>(r) / static_cast<unsigned>(page_rows);
         in_page = r - at * page_rows;
-        const int pg = __ldcg(table + static_cast<size_t>(b) * max_pages + at);
-        if (static_cast<unsigned>(pg) < static_cast<unsigned>(num_pages)) return pg;
+        return __ldcg(table + static_cast<size_t>(b) * max_pages + at);
+    }
+    // The page that an entry names; -1, with the error recorded, if it is none of the pool.  Nothing is read or
+    // written through such an entry.
+    __device__ __forceinline__ int page(int e) const {
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(num_pages)) return e;
         atomicOr(err, kErrBadPage);
         return -1;
     }
@@ -45,7 +49,7 @@ struct PageView {
     // a pool has more elements than 32 bits count.
     __device__ __forceinline__ long long pool_row(int b, int h, int r) const {
         int in_page;
-        const int pg = locate(b, r, in_page);
+        const int pg = page(entry(b, r, in_page));
         return pg < 0 ? -1 : (static_cast<long long>(pg) * kv_heads + h) * page_rows + in_page;
     }
 };

@@ -157,31 +157,37 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         test_producer_delay();
         const int boxes = kWeighKeys / p.box_rows;
         WeighWalk walk(p, stream);
-        int unit = 0, y = -1, z = 0;
+        // A tile ahead of the one being loaded: its unit, and lane's box of it (row in the page, -1 for none; the
+        // table's entry, on its way).
+        struct Ahead {
+            bool more;
+            int unit, y, e;
+        };
         auto look_up = [&]() {
-            if (!walk.next()) return false;
-            unit = walk.unit;
+            Ahead a;
+            a.more = walk.next();
+            a.unit = walk.unit;
+            a.y = -1;
+            a.e = 0;
             const int r = walk.t * kWeighKeys + lane * p.box_rows;
-            y = -1;
-            if (lane < boxes && r < walk.P) {
-                const int pg = p.pages.locate(walk.b, r, y);
-                z = pg < 0 ? p.pages.num_pages * Hkv : (p.pages.table == nullptr ? unit : pg * Hkv + unit % Hkv);
-            }
-            return true;
+            if (a.more && lane < boxes && r < walk.P) a.e = p.pages.entry(walk.b, r, a.y);
+            return a;
         };
         uint32_t it = 0, units = 0;
         int have = -1;
-        bool ok = true, more = look_up();
-        while (more && ok) {
-            const int cu = unit, cy = y, cz = z;
-            more = look_up();
-            if (cu != have) {
+        bool ok = true;
+        Ahead one = look_up(), two = look_up();
+        while (one.more) {
+            const Ahead now = one;
+            one = two;
+            two = look_up();
+            if (now.unit != have) {
                 const uint32_t qb = units % C::QB;
                 ok = wait_stage_warp(&q_empty[qb], ((units / C::QB) & 1) ^ 1, abort_flag, p.err);
                 if (!ok) break;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(&q_full[qb], n16 * D * 2);
-                    const int row = cu * p.rows + p.row0;  // packed rows of a unit are contiguous
+                    const int row = now.unit * p.rows + p.row0;  // packed rows of a unit are contiguous
                     for (int ch = 0; ch < C::NCH; ++ch)
                         for (int r = 0; r < n16; r += 16)
                             ptx::tma_load_2d(&p.tm_q, &q_full[qb], smem + C::OFF_Q + qb * C::Q_BYTES + ch * C::QCHUNK + r * C::RB,
@@ -189,7 +195,13 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
                 }
                 __syncwarp();
                 ++units;
-                have = cu;
+                have = now.unit;
+            }
+            const int cy = now.y;
+            int cz = now.unit;
+            if (cy >= 0 && p.pages.table != nullptr) {
+                const int pg = p.pages.page(now.e);
+                cz = (pg < 0 ? p.pages.num_pages : pg) * Hkv + (pg < 0 ? 0 : now.unit % Hkv);  // past the pool: zeros
             }
             const uint32_t st = it % C::NST;
             ok = wait_stage_warp(&k_empty[st], ((it / C::NST) & 1) ^ 1, abort_flag, p.err);
@@ -260,12 +272,12 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane;
         float* lse2 = reinterpret_cast<float*>(smem + C::OFF_LSE) + (warp - 4) * N;
         WeighWalk walk(p, stream);
-        // The tile ahead: its weight and whether a page backs it are on their way while this one's scores are waited
+        // The tile ahead: its weight and its table entry are on their way while this one's scores are waited
         // for.  at < 0: no row of this thread's.
         int unit_n = -1;
         long long at_n = -1;
         float before_n = 0.f;
-        bool backed_n = false;
+        int entry_n = 0;
         auto ahead = [&](int skip) {
             bool more = true;
             for (int i = 0; i <= skip && more; ++i) more = walk.next();
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
                 at_n = static_cast<long long>(unit_n) * cap + j;
                 before_n = __ldcg(p.weight + at_n);
                 int in_page;
-                backed_n = p.pages.locate(walk.b, j, in_page) >= 0;
+                entry_n = p.pages.entry(walk.b, j, in_page);
             }
             return true;
         };
@@ -287,7 +299,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             const int unit = unit_n;
             const long long at = at_n;
             const float before = before_n;
-            const bool backed = backed_n;
+            const int entry = entry_n;
             more = ahead(1);
             if (unit != have) {
                 have = unit;
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             }
             ptx::tc_fence_before();
             ptx::mbar_arrive(&s_free[g]);
-            if (at >= 0) p.weight_out[at] = before + (backed ? sum : 0.f);
+            if (at >= 0) p.weight_out[at] = before + (p.pages.page(entry) >= 0 ? sum : 0.f);
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(done);

@@ -374,33 +374,37 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 tma_load_4d(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(row0), 0);
             }
             __syncwarp();
-            // A batch of 32 look-ups, NB of each stage: cur covers the stages being issued, nxt those after.
+            // A batch of 32 look-ups, NB of each stage: cur covers the stages being issued, nxt those after, loaded
+            // but not looked at before their turn.
             constexpr int NB = KEYS / 16, SPB = 32 / NB;
             const int z_none = p.pages.num_pages * Hkv;  // past the pool: zeros are loaded
-            auto look_up = [&](int i, int& y, int& z) {  // box lane % NB of stage i: first row, pool index
+            auto look_up = [&](int i, int& y, int& e) {  // box lane % NB of stage i: row in its page, table entry
                 y = -1;
-                z = unit_b * Hkv + h;
+                e = 0;
                 const int c = c0 + i;
                 if (i >= n) return;
                 const int box = c < n_own ? p.own_box : p.box_rows, in = (lane % NB) * box;
                 const int r = (c < n_own ? c : c - n_own) * KEYS + in;
                 if (in >= KEYS || r >= (c < n_own ? own_rows : unit_P)) return;
                 y = r;
-                if (c >= n_own && p.pages.table != nullptr) {
-                    const int pg = p.pages.locate(unit_b, r, y);
-                    z = pg < 0 ? z_none : pg * Hkv + h;
-                }
+                if (c >= n_own) e = p.pages.entry(unit_b, r, y);
             };
-            int y_cur, z_cur, y_nxt = -1, z_nxt = 0;
-            look_up(lane / NB, y_cur, z_cur);
+            auto pool_index = [&](int i, int y, int e) {
+                if (y < 0 || c0 + i < n_own || p.pages.table == nullptr) return unit_b * Hkv + h;
+                const int pg = p.pages.page(e);
+                return pg < 0 ? z_none : pg * Hkv + h;
+            };
+            int y_cur = -1, z_cur = 0, y_nxt, e_nxt;
+            look_up(lane / NB, y_nxt, e_nxt);
             bool ok = true;
             int i = 0;
             uint32_t st = it % NST, use = it / NST;
             for (; i < n; ++i) {
                 const int in_batch = i % SPB;
                 if (in_batch == 0) {
-                    if (i > 0) y_cur = y_nxt, z_cur = z_nxt;
-                    look_up(i + SPB + lane / NB, y_nxt, z_nxt);
+                    y_cur = y_nxt;
+                    z_cur = pool_index(i + lane / NB, y_nxt, e_nxt);
+                    look_up(i + SPB + lane / NB, y_nxt, e_nxt);
                 }
                 const int y = __shfl_sync(0xffffffffu, y_cur, in_batch * NB + lane % NB);
                 const int z = __shfl_sync(0xffffffffu, z_cur, in_batch * NB + lane % NB);
