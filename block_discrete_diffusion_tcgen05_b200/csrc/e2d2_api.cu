@@ -24,6 +24,7 @@
 #include "kv_paged.cuh"
 #include "kv_weigh.cuh"
 #include "paged_attn.cuh"
+#include "paged_attn_tc.cuh"
 
 namespace e2d2 {
 
@@ -1006,6 +1007,22 @@ bool map_rows(CUtensorMap* m, const void* base, int D, long long rows, long long
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int N>
+e2d2_status launch_paged_tc(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
+    using C = TcCfg<N>;
+    auto kern = paged_attn_tc_kernel<N>;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC) != cudaSuccess)
+            return E2D2_ERR_CUDA;
+        configured_dev = dev;
+    }
+    const int grid = di->sms < kPagedMaxCtas ? di->sms : kPagedMaxCtas;
+    return launch_pdl(kern, dim3(grid), dim3(kTcThreads), C::ALLOC, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
+}
+
 template <int D>
 e2d2_status launch_paged_rows(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
     if (a.rows <= 16) return launch_paged<D, 1>(a, di, stream);
@@ -1127,16 +1144,21 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     PagedAttnParams a;
     const long long units = static_cast<long long>(pages.num_pages) * dims.kv_heads;
     a.rows = dims.q_heads / dims.kv_heads * S;
+    const bool tc = D == 128 && a.rows > kPagedTcRows;  // tensor-memory kernel
     const int rw = a.rows <= 16 ? 1 : (a.rows <= 32 ? 2 : 4);
-    const int keys = (D == 128 ? 64 : 128) / rw;  // of a stage
+    const int keys = tc ? kTcKeys : (D == 128 ? 64 : 128) / rw;  // of a stage
     a.box_rows = box_of(pages, keys);
     a.own_box = 16;
     while (a.own_box < S && a.own_box < keys) a.own_box *= 2;
-    bool ok = map_rows(&a.tm_q, q_blk, D, static_cast<long long>(dims.batch) * dims.q_heads * S, 1, 16 * rw) &&
-              map_rows(&a.tm_k, k_pages, D, pages.page_rows, units, a.box_rows) &&
-              map_rows(&a.tm_v, v_pages, D, pages.page_rows, units, a.box_rows);
-    if (ok && k_blk)
-        ok = map_rows(&a.tm_k1, k_blk, D, S, BHkv, a.own_box) && map_rows(&a.tm_v1, v_blk, D, S, BHkv, a.own_box);
+    bool ok = map_rows(&a.tm_q, q_blk, D, static_cast<long long>(dims.batch) * dims.q_heads * S, 1, 16 * rw);
+    if (tc)
+        ok = ok && map_3d(&a.tm_k, k_pages, D, pages.page_rows, units, pages.page_rows, a.box_rows) &&
+             map_3d(&a.tm_v, v_pages, D, pages.page_rows, units, pages.page_rows, a.box_rows) &&
+             (!k_blk || (map_3d(&a.tm_k1, k_blk, D, S, BHkv, S, a.own_box) && map_3d(&a.tm_v1, v_blk, D, S, BHkv, S, a.own_box)));
+    else
+        ok = ok && map_rows(&a.tm_k, k_pages, D, pages.page_rows, units, a.box_rows) &&
+             map_rows(&a.tm_v, v_pages, D, pages.page_rows, units, a.box_rows) &&
+             (!k_blk || (map_rows(&a.tm_k1, k_blk, D, S, BHkv, a.own_box) && map_rows(&a.tm_v1, v_blk, D, S, BHkv, a.own_box)));
     if (!ok) return E2D2_ERR_CUDA;
     if (!k_blk) a.tm_k1 = a.tm_k, a.tm_v1 = a.tm_v;
     a.pages = page_view(pages, dims, di);
@@ -1155,6 +1177,7 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     a.rows_cap = w.rows_cap;
     a.slot_floats = w.slot_floats;
     a.scale_log2 = scale_log2(dims);
+    if (tc) return a.rows <= 32 ? launch_paged_tc<32>(a, di, stream) : launch_paged_tc<64>(a, di, stream);
     switch (D) {
         case 32: return launch_paged_rows<32>(a, di, stream);
         case 64: return launch_paged_rows<64>(a, di, stream);

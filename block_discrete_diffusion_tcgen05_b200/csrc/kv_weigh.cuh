@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         ptx::tmem_alloc(holder, C::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    if (warp == 0) test_producer_delay();
     ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
     const int cap = p.pages.capacity(), Hkv = p.pages.kv_heads;
     const auto stream = entry_stream(p.P_dev, p.batch, cap, Hkv, [](int rows) { return weigh_tiles(rows); });
@@ -154,7 +155,6 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             ptx::tma_prefetch_desc(&p.tm_k);
             ptx::tma_prefetch_desc(&p.tm_q);
         }
-        test_producer_delay();
         const int boxes = kWeighKeys / p.box_rows;
         WeighWalk walk(p, stream);
         // A tile ahead of the one being loaded: its unit, and lane's box of it (row in the page, -1 for none; the

@@ -159,11 +159,11 @@ struct StreamCut {
     }
 };
 
-// Blocks that a call's stream is cut over: as many as keep about kPagedMinKeys keys each, one per unit at least, at
+// Blocks that a call's stream is cut over: as many as keep about min_stages stages each, one per unit at least, at
 // most the grid.  Units of equal length are cut into equal parts each, if that leaves no more than a fifth of the
 // blocks idle: a block whose range meets two units joins twice.
-__device__ __forceinline__ int paged_parts(unsigned total, unsigned units, bool equal, unsigned grid, int keys) {
-    const unsigned want = max(total / (kPagedMinKeys / keys), units);
+__device__ __forceinline__ int paged_parts(unsigned total, unsigned units, bool equal, unsigned grid, int min_stages) {
+    const unsigned want = max(total / min_stages, units);
     if (want >= grid) {
         if (equal && units <= grid) {
             const unsigned aligned = grid - grid % units;
@@ -186,20 +186,20 @@ __device__ __forceinline__ void write_row4(const PagedAttnParams& p, long long a
 // The last block of a shared unit: joins its parts, in the blocks' order, and writes the rows.  The first part's
 // slot, then one every two slots from `rest`.  D / 4 lanes per row, four columns each, IT rows and AT parts in flight;
 // lane k of a row's lanes takes part k's maximum and sum.  No shared memory, no barrier.
-template <int D, int IT, int AT>
+template <int D, int WARPS, int IT, int AT>
 __device__ __forceinline__ void join_parts(const PagedAttnParams& p, const float* first, const float* rest, int parts,
                                            long long row0, int rows, int warp, int lane) {
     constexpr int LPR = D / 4, RPW = 32 / LPR;
     const int li = lane % LPR;
     auto part = [&](int k) { return k == 0 ? first : rest + static_cast<size_t>(2 * (k - 1)) * p.slot_floats; };
 #pragma unroll 1
-    for (int base = warp * RPW; base < rows; base += 4 * RPW * IT) {
+    for (int base = warp * RPW; base < rows; base += WARPS * RPW * IT) {
         int row[IT];
         float mt[IT], lt[IT];
         float4 acc[IT];
 #pragma unroll
         for (int y = 0; y < IT; ++y) {
-            row[y] = min(base + 4 * RPW * y + lane / LPR, rows - 1);
+            row[y] = min(base + WARPS * RPW * y + lane / LPR, rows - 1);
             mt[y] = -INFINITY;
             lt[y] = 0.f;
             acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -257,13 +257,84 @@ __device__ __forceinline__ void join_parts(const PagedAttnParams& p, const float
         }
 #pragma unroll
         for (int y = 0; y < IT; ++y)
-            if (base + 4 * RPW * y + lane / LPR < rows) {
+            if (base + WARPS * RPW * y + lane / LPR < rows) {
                 write_row4(p, row0 + row[y], D, li, lt[y], acc[y]);
                 if (li == 0 && p.lse != nullptr)
                     p.lse[row0 + row[y]] = lt[y] > 0.f ? (mt[y] + log2f(lt[y])) * 0.69314718055994531f : -INFINITY;
             }
     }
 }
+
+// The units of a block: its range of the stream, unit by unit.  KEYS: of a stage; ROWS: of a unit; MIN_KEYS: that a
+// block of a cut unit should keep.  Every thread of a warp walks alike.
+template <int KEYS, int ROWS, int MIN_KEYS>
+struct PagedWalk {
+    const PagedAttnParams& p;
+    int upe, own_rows, n_own;     // units per entry; the own block's rows and stages
+    unsigned lead, pos, end, ent_beg, total;
+    int parts, next_b, next_P;
+    // the unit at hand: entry b with P rows, kv head h; its stages [c0, c0 + n) are this block's
+    int b, P, h, c0, n, rows_here;
+    long long row0;               // its first row in [B][Hq][S]
+    unsigned ubeg, len;           // its first place in the stream, its places
+    bool whole;                   // all of it is this block's
+
+    __device__ explicit PagedWalk(const PagedAttnParams& prm) : p(prm), pos(0), end(0) {
+        const int Hkv = p.pages.kv_heads;
+        upe = Hkv * p.qtiles;
+        own_rows = p.own ? p.S : 0;
+        n_own = (own_rows + KEYS - 1) / KEYS;
+        const int own = own_rows;
+        auto stream = entry_stream(p.P_dev, p.batch, p.pages.capacity(), upe,
+                                   [own](int rows) { return static_cast<unsigned>(max(1, paged_stages(rows, own, KEYS))); });
+        lead = stream.equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
+        stream.lead = lead;
+        total = stream.total + lead * p.batch * upe;
+        parts = paged_parts(total, p.batch * upe, stream.equal, gridDim.x, MIN_KEYS / KEYS);
+        if (idle()) return;
+        const StreamCut cut(total, parts);
+        pos = cut.begin(blockIdx.x);
+        end = cut.begin(blockIdx.x + 1);
+        stream.find(pos, next_b, ent_beg, next_P);
+    }
+    __device__ bool idle() const { return static_cast<int>(blockIdx.x) >= parts; }
+    __device__ bool next() {
+        while (pos < end) {
+            b = next_b;
+            P = next_P;
+            const int real = paged_stages(P, own_rows, KEYS), all = max(1, real);
+            len = lead + all;
+            const int u_in = (pos - ent_beg) / len;
+            ubeg = ent_beg + u_in * len;
+            const unsigned past = min(end - ubeg, len);
+            h = p.qtiles == 1 ? u_in : u_in / p.qtiles;
+            const int qt = u_in - h * p.qtiles;
+            c0 = max(static_cast<int>(pos - ubeg - lead), 0);
+            const int c1 = max(static_cast<int>(past - lead), 0);
+            pos = ubeg + past;
+            if (u_in + 1 == upe && past == len) {
+                ent_beg += upe * len;
+                ++next_b;
+                if (pos < end) next_P = ragged_clamp(__ldcg(p.P_dev + next_b), p.pages.capacity());
+            }
+            if (c0 == c1) continue;  // empty places only
+            whole = c0 == 0 && c1 == all;
+            n = max(0, min(c1, real) - c0);
+            rows_here = min(ROWS, p.rows - qt * ROWS);
+            row0 = (static_cast<long long>(b) * p.q_heads + static_cast<long long>(h) * p.group) * p.S +
+                   static_cast<long long>(qt) * ROWS;
+            return true;
+        }
+        return false;
+    }
+    // Blocks that share the unit: the first and the last with one of its stages.
+    __device__ int first_block() const { return StreamCut(total, parts).owner(ubeg + lead); }
+    __device__ int last_block() const { return StreamCut(total, parts).owner(ubeg + len - 1); }
+    // The slot of the unit's block c: a block begins one shared unit at most and goes on with one at most.
+    __device__ float* slot(int c, int first) const {
+        return p.partial + static_cast<size_t>(2 * c + (c == first)) * p.slot_floats;
+    }
+};
 
 template <int D, int RW>
 __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTAS)
@@ -300,27 +371,11 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
         ptx::tma_prefetch_desc(&p.tm_k);
         ptx::tma_prefetch_desc(&p.tm_v);
     }
+    if (loads) test_producer_delay();
     ptx::griddep_wait();  // lengths, table and rows are read after the previous kernel on the stream
 
-    // ---- schedule: this block's range of the stream and the entry it starts in
-    const int Hkv = p.pages.kv_heads, cap = p.pages.capacity();
-    const int upe = Hkv * p.qtiles;  // units per entry
-    const int own_rows = p.own ? p.S : 0;
-    const int n_own = (own_rows + KEYS - 1) / KEYS;
-    auto stream = entry_stream(p.P_dev, p.batch, cap, upe,
-                               [&](int rows) { return static_cast<unsigned>(max(1, paged_stages(rows, own_rows, KEYS))); });
-    const unsigned lead = stream.equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
-    if (lead > 0) {
-        stream.lead = lead;
-        stream.total += lead * p.batch * upe;
-    }
-    const StreamCut cut(stream.total, paged_parts(stream.total, p.batch * upe, stream.equal, gridDim.x, KEYS));
-    if (static_cast<int>(blockIdx.x) >= cut.parts) return;
-    unsigned pos = cut.begin(blockIdx.x), ent_beg;
-    const unsigned end = cut.begin(blockIdx.x + 1);
-    int b, P;
-    stream.find(pos, b, ent_beg, P);
-    if (loads) test_producer_delay();
+    PagedWalk<KEYS, ROWS, kPagedMinKeys> walk(p);
+    if (walk.idle()) return;
     __syncthreads();  // the barriers are initialised
 
     const int rw = warp % RW, slice = warp / RW;
@@ -341,29 +396,12 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     constexpr int SPC = C::RB / 32;  // steps per column chunk
     uint32_t it = 0, n_units = 0;    // stages that went through the ring so far, units
 
-    while (pos < end) {
-        // ---- the unit: entry b, kv head h, query tile qt; its stages [c0, c1) fall to this block
-        const int real = paged_stages(P, own_rows, KEYS);
-        const int Cu = max(1, real);
-        const unsigned len = lead + Cu;
-        const int u_in = (pos - ent_beg) / len;
-        const unsigned ubeg = ent_beg + u_in * len, past = min(end - ubeg, len);
-        const int h = p.qtiles == 1 ? u_in : u_in / p.qtiles, qt = u_in - h * p.qtiles;
-        const int c0 = max(static_cast<int>(pos - ubeg - lead), 0), c1 = max(static_cast<int>(past - lead), 0);
-        const bool whole = c0 == 0 && c1 == Cu;
-        pos = ubeg + past;
-        const int unit_b = b;
-        const int unit_P = P;
-        if (u_in + 1 == upe && past == len) {
-            ent_beg += upe * len;
-            ++b;
-            if (pos < end) P = ragged_clamp(__ldcg(p.P_dev + b), cap);
-        }
-        if (c0 == c1) continue;  // empty places only
-        const int rows_here = min(ROWS, p.rows - qt * ROWS);
-        const long long row0 = (static_cast<long long>(unit_b) * p.q_heads + static_cast<long long>(h) * p.group) * p.S +
-                               static_cast<long long>(qt) * ROWS;
-        const int n = max(0, min(c1, real) - c0);  // stages with keys
+    const int Hkv = p.pages.kv_heads;
+    while (walk.next()) {
+        const int unit_b = walk.b, unit_P = walk.P, h = walk.h, c0 = walk.c0, n = walk.n, rows_here = walk.rows_here;
+        const int n_own = walk.n_own, own_rows = walk.own_rows;
+        const bool whole = walk.whole;
+        const long long row0 = walk.row0;
 
         if (loads) {
             // ------------------------------------------------------------ loads
@@ -578,10 +616,8 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                     *reinterpret_cast<float2*>(dst + x * 8) = make_float2(o[x][2 * r] * f, o[x][2 * r + 1] * f);
             }
             ptx::named_barrier_sync(1, NCONS);
-            const int c_first = whole ? 0 : cut.owner(ubeg + lead);
-            // A block begins one shared unit at most and goes on with one at most: a slot for each.
-            auto slot_of = [&](int c) { return p.partial + static_cast<size_t>(2 * c + (c == c_first)) * p.slot_floats; };
-            float* slot = whole ? nullptr : slot_of(blockIdx.x);
+            const int c_first = whole ? 0 : walk.first_block();
+            float* slot = whole ? nullptr : walk.slot(blockIdx.x, c_first);
             for (int x = tid; x < rows_here * (D / 4); x += NCONS) {
                 const int row = x / (D / 4), q4 = x % (D / 4);
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -610,7 +646,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
             if (!whole) {
                 // publish; the last block of the unit joins all of them
                 ptx::named_barrier_sync(1, NCONS);
-                const int c_last = cut.owner(ubeg + len - 1);
+                const int c_last = walk.last_block();
                 if (tid == 0) {
                     __threadfence();
                     const int ticket = atomicAdd(&p.tickets[c_first], 1);
@@ -622,8 +658,8 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 if (*bcast) {
                     __threadfence();
                     const int parts = c_last - c_first + 1;
-                    if (rows_here <= 2 * C::WARPS * (128 / D)) join_parts<D, 1, 8>(p, slot_of(c_first), slot_of(c_first + 1), parts, row0, rows_here, warp, lane);
-                    else join_parts<D, 4, 2>(p, slot_of(c_first), slot_of(c_first + 1), parts, row0, rows_here, warp, lane);
+                    if (rows_here <= 2 * C::WARPS * (128 / D)) join_parts<D, C::WARPS, 1, 8>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), parts, row0, rows_here, warp, lane);
+                    else join_parts<D, C::WARPS, 4, 2>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), parts, row0, rows_here, warp, lane);
                 }
             }
         }

@@ -1,0 +1,475 @@
+// paged_attn_tc.cuh -- the paged sampling step for blocks of many query rows (17 to 64 share a kv head) at d = 128, on
+// the 5th-generation tensor cores.
+//
+// As paged_attn.cuh, but with the products taken transposed and their accumulators in tensor memory:
+//
+//     S^T  = K Q^T           M = 128 keys (lanes),  N columns = query rows,                  K = d
+//     O^T += V^T [P^T | R^T] M = d = 128 (lanes),   2 N columns = probabilities, remainders, K = keys
+//
+// P and R are the two bf16 that hold a probability to 16 bits and more: the remainders are N more columns of the same
+// product, added to the others' when the unit ends.  With mma.sync the rows' accumulators fill the registers from 32
+// rows on and few warps are left to hide its latencies; here a tile's softmax is 256 threads' (thread = key, warpgroup =
+// half of the columns) and the tensor cores work beside it.
+//
+// A column's running maximum is shared by its warpgroup's 128 keys: each tile the threads vote whether any key beats it
+// by more than 2^8, and only then is it reduced and the column of O^T rescaled.  Warp 0 loads Q and K, warp 2 loads V,
+// warp 1 issues S^T (two buffers: the next tile's is computed during this one's softmax), warp 3 issues O^T.  The rings
+// run ahead across units.  The cut of the work over blocks, the partial slots and the join are paged_attn.cuh's.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "fmha_keyrow_sm100.cuh"
+#include "paged_attn.cuh"
+
+namespace e2d2 {
+
+constexpr int kTcThreads = 384;   // 4 control warps, 2 softmax warpgroups
+constexpr int kTcKeys = 128;      // keys of a tile
+constexpr int kPagedTcRows = 16;  // query rows per kv head above which this kernel is taken (at d = 128)
+constexpr int kTcMinKeys = 384;   // keys per block that the split aims for
+
+template <int N_>
+struct TcCfg {
+    static constexpr int N = N_, D = 128;
+    static constexpr int NH = N / 2;                  // columns per warpgroup
+    static constexpr int KV = kTcKeys * D * 2;        // K (or V) of a tile: two column halves of 128-byte rows
+    static constexpr int HALF = kTcKeys * 128;
+    static constexpr int Q_BYTES = N * D * 2;
+    static constexpr int P_CHUNKS = 2 * N / 64;       // 64-column chunks of [P^T | R^T]
+    static constexpr int P_BYTES = P_CHUNKS * HALF;
+    static constexpr int NK = N == 64 ? 2 : 3, NV = 3;
+    static constexpr uint32_t TMEM_COLS = 4 * N;      // S^T at 0 and N, O^T at 2 N
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_P = OFF_Q + Q_BYTES;
+    static constexpr int OFF_K = OFF_P + P_BYTES;
+    static constexpr int OFF_V = OFF_K + NK * KV;
+    static constexpr int OFF_BAR = OFF_V + NV * KV;
+    // q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[2], s_free[2], p_full, pv_done, o_free,
+    // s_drain, pv_drain, done
+    static constexpr int NBAR = 2 + 2 * NK + 2 * NV + 4 + 6;
+    static constexpr int OFF_VOTE = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // u32 [2 wg][2 parity][4 warps]
+    static constexpr int OFF_CMAX = OFF_VOTE + 64;                        // float [2 wg][2 parity][4 warps][NH]
+    static constexpr int OFF_LRED = OFF_CMAX + 2 * 2 * 4 * NH * 4;        // float [2 wg][4 warps][NH]
+    static constexpr int OFF_MISC = OFF_LRED + 2 * 4 * NH * 4;            // holder, abort, broadcast
+    static constexpr int ALLOC = OFF_MISC + 16 + 1024;                    // + alignment slack
+    static_assert(ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
+};
+
+template <int N>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnParams p) {
+    using C = TcCfg<N>;
+    constexpr int NH = C::NH, D = C::D;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* k_full = q_empty + 1;
+    uint64_t* k_empty = k_full + C::NK;
+    uint64_t* v_full = k_empty + C::NK;
+    uint64_t* v_empty = v_full + C::NV;
+    uint64_t* s_full = v_empty + C::NV;
+    uint64_t* s_free = s_full + 2;
+    uint64_t* p_full = s_free + 2;
+    uint64_t* pv_done = p_full + 1;
+    uint64_t* o_free = pv_done + 1;
+    uint64_t* s_drain = o_free + 1;
+    uint64_t* pv_drain = s_drain + 1;
+    uint64_t* done = pv_drain + 1;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    volatile int* bcast = abort_flag + 1;
+
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(q_empty, 1);
+        for (int i = 0; i < C::NK; ++i) ptx::mbar_init(&k_full[i], 1), ptx::mbar_init(&k_empty[i], 1);
+        for (int i = 0; i < C::NV; ++i) ptx::mbar_init(&v_full[i], 1), ptx::mbar_init(&v_empty[i], 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 256);
+        ptx::mbar_init(p_full, 256);
+        ptx::mbar_init(pv_done, 1);
+        ptx::mbar_init(o_free, 256);
+        ptx::mbar_init(s_drain, 1);
+        ptx::mbar_init(pv_drain, 1);
+        ptx::mbar_init(done, 256);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(holder, C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    if (warp == 0 || warp == 2) {
+        if (lane == 0) {
+            ptx::tma_prefetch_desc(warp == 0 ? &p.tm_k : &p.tm_v);
+            ptx::tma_prefetch_desc(warp == 0 ? &p.tm_k1 : &p.tm_v1);
+            if (warp == 0) ptx::tma_prefetch_desc(&p.tm_q);
+        }
+        test_producer_delay();
+    }
+    ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *holder;
+    const int Hkv = p.pages.kv_heads;
+    PagedWalk<kTcKeys, N, kTcMinKeys> walk(p);  // an idle block's has no units: its roles fall through
+    // rows of tile c of the unit at hand, and whether it is the own block's
+    auto tile_rows = [&](int c, bool& is_own) {
+        is_own = c < walk.n_own;
+        return (is_own ? walk.own_rows - c * kTcKeys : walk.P - (c - walk.n_own) * kTcKeys);
+    };
+
+    if (warp == 0 || warp == 2) {
+        // ---------------------------------------------------------------- loads: warp 0 Q and K, warp 2 V
+        const bool is_k = warp == 0;
+        const int NS = is_k ? C::NK : C::NV;
+        uint64_t* full = is_k ? k_full : v_full;
+        uint64_t* empty = is_k ? k_empty : v_empty;
+        uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+        uint32_t it = 0, units = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            if (walk.n == 0) continue;
+            if (is_k) {
+                ok = wait_stage_warp(q_empty, (units & 1) ^ 1, abort_flag, p.err);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+                    tma_load_4d(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(walk.row0), 0);
+                }
+                __syncwarp();
+            }
+            ++units;
+            // lane j: box j of a tile, its table entry on its way a tile ahead
+            auto look_up = [&](int i, int& y, int& e) {
+                y = -1;
+                e = 0;
+                const int c = walk.c0 + i;
+                if (i >= walk.n) return;
+                const int box = c < walk.n_own ? p.own_box : p.box_rows, in = lane * box;
+                const int r = (c < walk.n_own ? c : c - walk.n_own) * kTcKeys + in;
+                if (in >= kTcKeys || r >= (c < walk.n_own ? walk.own_rows : walk.P)) return;
+                y = r;
+                if (c >= walk.n_own) e = p.pages.entry(walk.b, r, y);
+            };
+            int y_nxt, e_nxt;
+            look_up(0, y_nxt, e_nxt);
+            for (int i = 0; i < walk.n; ++i) {
+                const int y = y_nxt, e = e_nxt;
+                look_up(i + 1, y_nxt, e_nxt);
+                const bool is_own = walk.c0 + i < walk.n_own;
+                const int box = is_own ? p.own_box : p.box_rows;
+                int z = walk.b * Hkv + walk.h;
+                if (y >= 0 && !is_own && p.pages.table != nullptr) {
+                    const int pg = p.pages.page(e);
+                    z = pg < 0 ? p.pages.num_pages * Hkv : pg * Hkv + walk.h;  // past the pool: zeros
+                }
+                const uint32_t st = it % NS;
+                ok = wait_stage_warp(&empty[st], ((it / NS) & 1) ^ 1, abort_flag, p.err);
+                if (!ok) break;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, y >= 0));
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(boxes) * box * D * 2);
+                __syncwarp();
+                if (y >= 0) {
+                    const CUtensorMap* map = is_k ? (is_own ? &p.tm_k1 : &p.tm_k) : (is_own ? &p.tm_v1 : &p.tm_v);
+                    uint8_t* dst = ring + st * C::KV + lane * box * 128;
+                    ptx::tma_load_3d(map, &full[st], dst, 0, y, z);
+                    ptx::tma_load_3d(map, &full[st], dst + C::HALF, 64, y, z);
+                }
+                __syncwarp();
+                ++it;
+            }
+        }
+        // never leave with copies in flight
+        volatile int no_abort = 0;
+        for (uint32_t i = it > static_cast<uint32_t>(NS) ? it - NS : 0u; i < it; ++i)
+            wait_bar_warp(&full[i % NS], (i / NS) & 1, &no_abort, p.err, true);
+        if (is_k && units > 0) wait_bar_warp(q_full, (units - 1) & 1, &no_abort, p.err, true);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- S^T = K Q^T
+        const bool leader = ptx::elect_one();
+        const uint32_t sQ = ptx::smem_u32(smem + C::OFF_Q), sK = ptx::smem_u32(smem + C::OFF_K);
+        const uint64_t desc = ptx::smem_desc(0, 16, 1024, 2u);  // K (A) and Q (B): K-major, 128-byte swizzle
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTcKeys, N, false, false);
+        uint32_t it = 0, units = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            if (walk.n == 0) continue;
+            ok = wait_stage_warp(q_full, units & 1, abort_flag, p.err);
+            ++units;
+            for (int i = 0; i < walk.n && ok; ++i) {
+                const uint32_t st = it % C::NK, sb = it & 1;
+                ok = wait_stage_warp(&s_free[sb], ((it >> 1) & 1) ^ 1, abort_flag, p.err) &&
+                     wait_stage_warp(&k_full[st], (it / C::NK) & 1, abort_flag, p.err);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint32_t k = sK + st * C::KV;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        ptx::mma_ss(tmem + sb * N, desc | ((k + (ks / 4) * C::HALF + (ks % 4) * 32) >> 4),
+                                    desc | ((sQ + (ks / 4) * (N * 128) + (ks % 4) * 32) >> 4), idesc, ks > 0 ? 1u : 0u);
+                    ptx::mma_commit(&k_empty[st]);
+                    ptx::mma_commit(&s_full[sb]);
+                    if (i == walk.n - 1) ptx::mma_commit(q_empty);
+                }
+                __syncwarp();
+                ++it;
+            }
+        }
+        // tensor memory is released when both issuers' products and every softmax thread are done
+        if (leader) ptx::mma_commit(s_drain);
+        __syncwarp();
+        volatile int no_abort = 0;
+        wait_bar_warp(s_drain, 0, &no_abort, p.err, true);
+        wait_bar_warp(pv_drain, 0, &no_abort, p.err, true);
+        wait_bar_warp(done, 0, &no_abort, p.err, true);
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- O^T += V^T [P^T | R^T]
+        const bool leader = ptx::elect_one();
+        const uint32_t sP = ptx::smem_u32(smem + C::OFF_P), sV = ptx::smem_u32(smem + C::OFF_V);
+        const uint64_t desc = ptx::smem_desc(0, C::HALF, 1024, 2u);  // both MN-major: V^T (d contiguous), P^T (columns)
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(D, 2 * N, true, true);
+        uint32_t it = 0, units = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            if (walk.n == 0) continue;
+            for (int i = 0; i < walk.n && ok; ++i) {
+                const uint32_t st = it % C::NV;
+                ok = wait_stage_warp(p_full, it & 1, abort_flag, p.err) &&
+                     (i > 0 || wait_stage_warp(o_free, (units & 1) ^ 1, abort_flag, p.err)) &&
+                     wait_stage_warp(&v_full[st], (it / C::NV) & 1, abort_flag, p.err);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                bool is_own;
+                const int steps = (min(kTcKeys, tile_rows(walk.c0 + i, is_own)) + 15) / 16;
+                if (leader) {
+                    const uint32_t v = sV + st * C::KV;
+                    for (int ks = 0; ks < steps; ++ks)
+                        ptx::mma_ss(tmem + 2 * N, desc | ((v + ks * 16 * 128) >> 4), desc | ((sP + ks * 16 * 128) >> 4), idesc,
+                                    i > 0 || ks > 0 ? 1u : 0u);
+                    ptx::mma_commit(&v_empty[st]);
+                    ptx::mma_commit(pv_done);
+                }
+                __syncwarp();
+                ++it;
+            }
+            ++units;
+        }
+        if (leader) ptx::mma_commit(pv_drain);
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax: thread = key lane, warpgroup = columns
+        // Waits never break the loops: every warp takes every named barrier.
+        const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane, tid = threadIdx.x - 128;
+        const uint32_t lane_off = static_cast<uint32_t>(32 * w) << 16;
+        const uint32_t o_tmem = tmem + lane_off + 2 * N + g * NH;  // this half's probabilities; remainders N columns on
+        uint32_t* vote = reinterpret_cast<uint32_t*>(smem + C::OFF_VOTE) + g * 8;
+        float* cmax = reinterpret_cast<float*>(smem + C::OFF_CMAX) + g * 2 * 4 * NH;
+        float* lred = reinterpret_cast<float*>(smem + C::OFF_LRED) + g * 4 * NH;
+        uint8_t* sP = smem + C::OFF_P;
+        uint32_t tc = 0;
+        while (walk.next()) {
+            float m_run[NH], l_part[NH];
+#pragma unroll
+            for (int j = 0; j < NH; ++j) m_run[j] = -INFINITY, l_part[j] = 0.f;
+            // the table's entry for this thread's key, on its way a tile ahead
+            auto entry_of = [&](int i) {
+                const int c = walk.c0 + i, j = (c - walk.n_own) * kTcKeys + key;
+                int in_page;
+                return i < walk.n && c >= walk.n_own && j < walk.P ? p.pages.entry(walk.b, j, in_page) : 0;
+            };
+            int e_nxt = entry_of(0);
+            for (int i = 0; i < walk.n; ++i, ++tc) {
+                const uint32_t sb = tc & 1;
+                const int e = e_nxt;
+                e_nxt = entry_of(i + 1);
+                bool is_own;
+                const int valid = tile_rows(walk.c0 + i, is_own);
+                bool key_ok = key < valid;
+                if (key_ok && !is_own) key_ok = p.pages.page(e) >= 0;
+                wait_stage_warp(&s_full[sb], (tc >> 1) & 1, abort_flag, p.err);
+                ptx::tc_fence_after();
+                float x[NH];
+                {
+                    uint32_t raw[NH];
+                    tmem_ld_cols<NH>(tmem + sb * N + lane_off + g * NH, raw);
+                    ptx::tmem_wait_ld();
+                    ptx::reg_fence<NH>(raw);
+#pragma unroll
+                    for (int j = 0; j < NH; ++j) x[j] = key_ok ? __uint_as_float(raw[j]) * p.scale_log2 : -INFINITY;
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&s_free[sb]);  // the next S^T product may overwrite the buffer
+                // Vote: does any key of the tile beat a column's running max by more than 2^8?
+                uint32_t v = 0;
+#pragma unroll
+                for (int j = 0; j < NH; ++j) v |= (x[j] > m_run[j] + kRescaleThreshold) ? (1u << j) : 0u;
+                v = __reduce_or_sync(0xffffffffu, v);
+                if (lane == 0) vote[sb * 4 + w] = v;
+                ptx::named_barrier_sync(1 + g, 128);
+                const uint4 vv = *reinterpret_cast<const uint4*>(vote + sb * 4);
+                const uint32_t E = vv.x | vv.y | vv.z | vv.w;
+                bool waited = tc == 0;  // the last tile's product has read P^T and landed in O^T
+                if (E != 0) {
+                    float tmp[NH];
+#pragma unroll
+                    for (int j = 0; j < NH; ++j) tmp[j] = x[j];
+                    const float mine = warp_columns_reduce<NH>(tmp, lane, [](float a, float b) { return fmaxf(a, b); });
+                    float* cm = cmax + sb * 4 * NH;
+                    if ((lane % (32 / NH)) == 0) cm[w * NH + lane / (32 / NH)] = mine;
+                    ptx::named_barrier_sync(1 + g, 128);
+                    if (!waited) {
+                        wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
+                        ptx::tc_fence_after();
+                        waited = true;
+                    }
+                    // eight columns at a time: the new max where the vote moved it, the factor 2^(old - new)
+#pragma unroll
+                    for (int c8 = 0; c8 < NH; c8 += 8) {
+                        float fac[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int j = c8 + k;
+                            const float tm = fmaxf(fmaxf(cm[j], cm[NH + j]), fmaxf(cm[2 * NH + j], cm[3 * NH + j]));
+                            const float mn = ((E >> j) & 1u) ? tm : m_run[j];
+                            fac[k] = ptx::ex2(mn == m_run[j] ? 0.f : m_run[j] - mn);
+                            m_run[j] = mn;
+                            l_part[j] *= fac[k];
+                        }
+                        if (i > 0 && ((E >> c8) & 0xffu) != 0) {
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {  // probabilities, remainders
+                                uint32_t o[8];
+                                ptx::tmem_ld8(o_tmem + part * N + c8, o);
+                                ptx::tmem_wait_ld();
+                                ptx::reg_fence<8>(o);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac[k]);
+                                ptx::tmem_st8(o_tmem + part * N + c8, o);
+                            }
+                        }
+                    }
+                    if (i > 0) ptx::tmem_wait_st();
+                }
+                // this key's row of [P^T | R^T]: exp2(x - m) as bf16 and bf16 remainder
+                uint32_t hi[NH / 2], lo[NH / 2];
+#pragma unroll
+                for (int j = 0; j < NH; j += 2) {
+                    const float e0 = m_run[j] == -INFINITY ? 0.f : ptx::ex2(x[j] - m_run[j]);
+                    const float e1 = m_run[j + 1] == -INFINITY ? 0.f : ptx::ex2(x[j + 1] - m_run[j + 1]);
+                    l_part[j] += e0;
+                    l_part[j + 1] += e1;
+                    const uint32_t h2 = ptx::pack_bf16x2(e0, e1);
+                    hi[j / 2] = h2;
+                    lo[j / 2] = ptx::pack_bf16x2(e0 - __uint_as_float(h2 << 16), e1 - __uint_as_float(h2 & 0xffff0000u));
+                }
+                if (!waited) wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
+#pragma unroll
+                for (int u = 0; u < NH / 8; ++u) {
+                    const int uh = g * (NH / 8) + u, ul = N / 8 + uh;  // 16-byte units of the row
+                    *reinterpret_cast<uint4*>(sP + uh / 8 * C::HALF + swz_rows<128>(key, uh % 8)) =
+                        make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+                    *reinterpret_cast<uint4*>(sP + ul / 8 * C::HALF + swz_rows<128>(key, ul % 8)) =
+                        make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+                }
+                if (g == 0 && !is_own && valid < kTcKeys && (valid & 15) != 0) {
+                    // Rows past the length in the last 16 keys that the product takes may hold anything (NaN
+                    // included), and meet zero probabilities: they become zero.
+                    const uint32_t st = tc % C::NV;
+                    wait_stage_warp(&v_full[st], (tc / C::NV) & 1, abort_flag, p.err);
+                    if (key >= valid && key < ((valid + 15) & ~15)) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::KV + half * C::HALF + key * 128);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(p_full);
+            }
+            // ---- the unit's end: column sums over the keys, O^T out of tensor memory
+            const bool whole = walk.whole;
+            const int rows_here = walk.rows_here;
+            const int c_first = whole ? 0 : walk.first_block();
+            float* slot = whole ? nullptr : walk.slot(blockIdx.x, c_first);
+            if (walk.n > 0) {
+                const float mine = warp_columns_reduce<NH>(l_part, lane, [](float a, float b) { return a + b; });
+                if ((lane % (32 / NH)) == 0) lred[w * NH + lane / (32 / NH)] = mine;
+                ptx::named_barrier_sync(1 + g, 128);
+                wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
+                ptx::tc_fence_after();
+            }
+#pragma unroll
+            for (int c8 = 0; c8 < NH; c8 += 8) {
+                uint32_t oh[8], ol[8];
+                if (walk.n > 0) {
+                    ptx::tmem_ld8(o_tmem + c8, oh);
+                    ptx::tmem_ld8(o_tmem + N + c8, ol);
+                    ptx::tmem_wait_ld();
+                    ptx::reg_fence<8>(oh);
+                    ptx::reg_fence<8>(ol);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) oh[k] = ol[k] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int j = c8 + k, col = g * NH + j;
+                    if (col >= rows_here) continue;
+                    const float o = __uint_as_float(oh[k]) + __uint_as_float(ol[k]);
+                    const float l = walk.n > 0 ? (lred[j] + lred[NH + j]) + (lred[2 * NH + j] + lred[3 * NH + j]) : 0.f;
+                    if (whole) {
+                        p.out[(walk.row0 + col) * D + key] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+                        if (key == 0 && p.lse != nullptr)
+                            p.lse[walk.row0 + col] = l > 0.f ? (m_run[j] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    } else {
+                        __stcg(slot + col * D + key, o);
+                        if (key == 0) {
+                            __stcg(slot + p.rows_cap * D + col, m_run[j]);
+                            __stcg(slot + p.rows_cap * D + p.rows_cap + col, l);
+                        }
+                    }
+                }
+            }
+            if (walk.n > 0) {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(o_free);
+            }
+            if (!whole) {
+                // publish; the last block of the unit joins all of them
+                ptx::named_barrier_sync(3, 256);
+                const int c_last = walk.last_block();
+                if (tid == 0) {
+                    __threadfence();
+                    const int ticket = atomicAdd(&p.tickets[c_first], 1);
+                    const int last = ticket == c_last - c_first;
+                    if (last) p.tickets[c_first] = 0;
+                    *bcast = last;
+                }
+                ptx::named_barrier_sync(3, 256);
+                const bool join = *bcast != 0;
+                ptx::named_barrier_sync(3, 256);  // read before the next unit's is written
+                if (join) {
+                    __threadfence();
+                    join_parts<D, 8, 4, 2>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
+                                           walk.row0, rows_here, warp - 4, lane);
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(done);
+    }
+}
+
+}  // namespace e2d2
