@@ -1020,7 +1020,7 @@ e2d2_status launch_paged_tc(const PagedAttnParams& a, const DeviceInfo* di, cuda
         configured_dev = dev;
     }
     const int grid = di->sms < kPagedMaxCtas ? di->sms : kPagedMaxCtas;
-    return launch_pdl(kern, dim3(grid), dim3(kTcThreads), C::ALLOC, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
+    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::ALLOC, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
 }
 
 template <int D>

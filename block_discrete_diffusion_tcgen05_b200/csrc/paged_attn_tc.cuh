@@ -8,11 +8,12 @@
 //
 // P and R are the two bf16 that hold a probability to 16 bits and more: the remainders are N more columns of the same
 // product, added to the others' when the unit ends.  With mma.sync the rows' accumulators fill the registers from 32
-// rows on and few warps are left to hide its latencies; here a tile's softmax is 256 threads' (thread = key, warpgroup =
-// half of the columns) and the tensor cores work beside it.
+// rows on and few warps are left to hide its latencies; here a tile's softmax is that of 128 threads for every
+// 16 columns (thread = key) and the tensor cores work beside it.
 //
-// A column's running maximum is shared by its warpgroup's 128 keys: each tile the threads vote whether any key beats it
-// by more than 2^8, and only then is it reduced and the column of O^T rescaled.  Warp 0 loads Q and K, warp 2 loads V,
+// A column's running maximum is shared by its warpgroup's 128 keys: each tile the threads vote whether any key beats
+// any of their columns' by more than 2^8, and only then are they reduced and O^T rescaled.  It is held negated and in
+// the exponent's units, so that one multiply-add gives both the vote's and the exponential's argument.  Warp 0 loads Q and K, warp 2 loads V,
 // warp 1 issues S^T (two buffers: the next tile's is computed during this one's softmax), warp 3 issues O^T.  The rings
 // run ahead across units.  The cut of the work over blocks, the partial slots and the join are paged_attn.cuh's.
 #pragma once
@@ -26,7 +27,6 @@
 
 namespace e2d2 {
 
-constexpr int kTcThreads = 384;   // 4 control warps, 2 softmax warpgroups
 constexpr int kTcKeys = 128;      // keys of a tile
 constexpr int kPagedTcRows = 16;  // query rows per kv head above which this kernel is taken (at d = 128)
 constexpr int kTcMinKeys = 384;   // keys per block that the split aims for
@@ -34,7 +34,9 @@ constexpr int kTcMinKeys = 384;   // keys per block that the split aims for
 template <int N_>
 struct TcCfg {
     static constexpr int N = N_, D = 128;
-    static constexpr int NH = N / 2;                  // columns per warpgroup
+    static constexpr int NH = 16;                     // columns per softmax warpgroup
+    static constexpr int WGS = N / NH, SOFT = 128 * WGS;  // warpgroups, their threads
+    static constexpr int THREADS = 128 + SOFT;        // and four control warps
     static constexpr int KV = kTcKeys * D * 2;        // K (or V) of a tile: two column halves of 128-byte rows
     static constexpr int HALF = kTcKeys * 128;
     static constexpr int Q_BYTES = N * D * 2;
@@ -50,16 +52,29 @@ struct TcCfg {
     // q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[2], s_free[2], p_full, pv_done, o_free,
     // s_drain, pv_drain, done
     static constexpr int NBAR = 2 + 2 * NK + 2 * NV + 4 + 6;
-    static constexpr int OFF_VOTE = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // u32 [2 wg][2 parity][4 warps]
-    static constexpr int OFF_CMAX = OFF_VOTE + 64;                        // float [2 wg][2 parity][4 warps][NH]
-    static constexpr int OFF_LRED = OFF_CMAX + 2 * 2 * 4 * NH * 4;        // float [2 wg][4 warps][NH]
-    static constexpr int OFF_MISC = OFF_LRED + 2 * 4 * NH * 4;            // holder, abort, broadcast
+    static constexpr int OFF_CMAX = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // float [WGS][2 parity][4 warps][NH]
+    static constexpr int OFF_LRED = OFF_CMAX + WGS * 2 * 4 * NH * 4;      // float [WGS][4 warps][NH]
+    static constexpr int OFF_MISC = OFF_LRED + WGS * 4 * NH * 4;          // holder, abort, broadcast
     static constexpr int ALLOC = OFF_MISC + 16 + 1024;                    // + alignment slack
     static_assert(ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
 };
 
+// Named barrier of n threads that also says whether any of them brought true.
+__device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t n, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(any)
+        : "r"(mine ? 1u : 0u), "r"(id), "r"(n)
+        : "memory");
+    return any != 0;
+}
+
 template <int N>
-__global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnParams p) {
     using C = TcCfg<N>;
     constexpr int NH = C::NH, D = C::D;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -89,13 +104,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         ptx::mbar_init(q_empty, 1);
         for (int i = 0; i < C::NK; ++i) ptx::mbar_init(&k_full[i], 1), ptx::mbar_init(&k_empty[i], 1);
         for (int i = 0; i < C::NV; ++i) ptx::mbar_init(&v_full[i], 1), ptx::mbar_init(&v_empty[i], 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 256);
-        ptx::mbar_init(p_full, 256);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], C::SOFT);
+        ptx::mbar_init(p_full, C::SOFT);
         ptx::mbar_init(pv_done, 1);
-        ptx::mbar_init(o_free, 256);
+        ptx::mbar_init(o_free, C::SOFT);
         ptx::mbar_init(s_drain, 1);
         ptx::mbar_init(pv_drain, 1);
-        ptx::mbar_init(done, 256);
+        ptx::mbar_init(done, C::SOFT);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -270,16 +285,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         // Waits never break the loops: every warp takes every named barrier.
         const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane, tid = threadIdx.x - 128;
         const uint32_t lane_off = static_cast<uint32_t>(32 * w) << 16;
-        const uint32_t o_tmem = tmem + lane_off + 2 * N + g * NH;  // this half's probabilities; remainders N columns on
-        uint32_t* vote = reinterpret_cast<uint32_t*>(smem + C::OFF_VOTE) + g * 8;
+        const uint32_t o_tmem = tmem + lane_off + 2 * N + g * NH;  // these columns' probabilities; remainders N columns on
         float* cmax = reinterpret_cast<float*>(smem + C::OFF_CMAX) + g * 2 * 4 * NH;
         float* lred = reinterpret_cast<float*>(smem + C::OFF_LRED) + g * 4 * NH;
         uint8_t* sP = smem + C::OFF_P;
+        constexpr float kNone = 3.0e38f;  // -(maximum) of a column without keys: finite, so that -inf scores give 0
         uint32_t tc = 0;
         while (walk.next()) {
-            float m_run[NH], l_part[NH];
+            float neg_m[NH], l_part[NH];
 #pragma unroll
-            for (int j = 0; j < NH; ++j) m_run[j] = -INFINITY, l_part[j] = 0.f;
+            for (int j = 0; j < NH; ++j) neg_m[j] = kNone, l_part[j] = 0.f;
             // the table's entry for this thread's key, on its way a tile ahead
             auto entry_of = [&](int i) {
                 const int c = walk.c0 + i, j = (c - walk.n_own) * kTcKeys + key;
@@ -300,28 +315,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 float x[NH];
                 {
                     uint32_t raw[NH];
-                    tmem_ld_cols<NH>(tmem + sb * N + lane_off + g * NH, raw);
+                    ptx::tmem_ld16(tmem + sb * N + lane_off + g * NH, raw);
                     ptx::tmem_wait_ld();
                     ptx::reg_fence<NH>(raw);
 #pragma unroll
-                    for (int j = 0; j < NH; ++j) x[j] = key_ok ? __uint_as_float(raw[j]) * p.scale_log2 : -INFINITY;
+                    for (int j = 0; j < NH; ++j) x[j] = __uint_as_float(raw[j]);
                 }
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&s_free[sb]);  // the next S^T product may overwrite the buffer
-                // Vote: does any key of the tile beat a column's running max by more than 2^8?
-                uint32_t v = 0;
+                if (!key_ok)
 #pragma unroll
-                for (int j = 0; j < NH; ++j) v |= (x[j] > m_run[j] + kRescaleThreshold) ? (1u << j) : 0u;
-                v = __reduce_or_sync(0xffffffffu, v);
-                if (lane == 0) vote[sb * 4 + w] = v;
-                ptx::named_barrier_sync(1 + g, 128);
-                const uint4 vv = *reinterpret_cast<const uint4*>(vote + sb * 4);
-                const uint32_t E = vv.x | vv.y | vv.z | vv.w;
+                    for (int j = 0; j < NH; ++j) x[j] = -INFINITY;
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < NH; ++j) top = fmaxf(top, fmaf(x[j], p.scale_log2, neg_m[j]));
                 bool waited = tc == 0;  // the last tile's product has read P^T and landed in O^T
-                if (E != 0) {
+                if (barrier_any(1 + g, 128, top > kRescaleThreshold)) {
+                    // new maxima, of every column whose keys reach past the old one
                     float tmp[NH];
 #pragma unroll
-                    for (int j = 0; j < NH; ++j) tmp[j] = x[j];
+                    for (int j = 0; j < NH; ++j) tmp[j] = x[j] * p.scale_log2;
                     const float mine = warp_columns_reduce<NH>(tmp, lane, [](float a, float b) { return fmaxf(a, b); });
                     float* cm = cmax + sb * 4 * NH;
                     if ((lane % (32 / NH)) == 0) cm[w * NH + lane / (32 / NH)] = mine;
@@ -331,7 +344,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         ptx::tc_fence_after();
                         waited = true;
                     }
-                    // eight columns at a time: the new max where the vote moved it, the factor 2^(old - new)
 #pragma unroll
                     for (int c8 = 0; c8 < NH; c8 += 8) {
                         float fac[8];
@@ -339,12 +351,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         for (int k = 0; k < 8; ++k) {
                             const int j = c8 + k;
                             const float tm = fmaxf(fmaxf(cm[j], cm[NH + j]), fmaxf(cm[2 * NH + j], cm[3 * NH + j]));
-                            const float mn = ((E >> j) & 1u) ? tm : m_run[j];
-                            fac[k] = ptx::ex2(mn == m_run[j] ? 0.f : m_run[j] - mn);
-                            m_run[j] = mn;
+                            const float nm = fminf(neg_m[j], tm == -INFINITY ? kNone : -tm);
+                            fac[k] = ptx::ex2(nm - neg_m[j]);
+                            neg_m[j] = nm;
                             l_part[j] *= fac[k];
                         }
-                        if (i > 0 && ((E >> c8) & 0xffu) != 0) {
+                        if (i > 0) {
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {  // probabilities, remainders
                                 uint32_t o[8];
@@ -363,8 +375,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 uint32_t hi[NH / 2], lo[NH / 2];
 #pragma unroll
                 for (int j = 0; j < NH; j += 2) {
-                    const float e0 = m_run[j] == -INFINITY ? 0.f : ptx::ex2(x[j] - m_run[j]);
-                    const float e1 = m_run[j + 1] == -INFINITY ? 0.f : ptx::ex2(x[j + 1] - m_run[j + 1]);
+                    const float e0 = ptx::ex2(fmaf(x[j], p.scale_log2, neg_m[j]));
+                    const float e1 = ptx::ex2(fmaf(x[j + 1], p.scale_log2, neg_m[j + 1]));
                     l_part[j] += e0;
                     l_part[j + 1] += e1;
                     const uint32_t h2 = ptx::pack_bf16x2(e0, e1);
@@ -432,11 +444,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     if (whole) {
                         p.out[(walk.row0 + col) * D + key] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
                         if (key == 0 && p.lse != nullptr)
-                            p.lse[walk.row0 + col] = l > 0.f ? (m_run[j] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                            p.lse[walk.row0 + col] = l > 0.f ? (log2f(l) - neg_m[j]) * 0.69314718055994531f : -INFINITY;
                     } else {
                         __stcg(slot + col * D + key, o);
                         if (key == 0) {
-                            __stcg(slot + p.rows_cap * D + col, m_run[j]);
+                            __stcg(slot + p.rows_cap * D + col, l > 0.f ? -neg_m[j] : -INFINITY);
                             __stcg(slot + p.rows_cap * D + p.rows_cap + col, l);
                         }
                     }
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             }
             if (!whole) {
                 // publish; the last block of the unit joins all of them
-                ptx::named_barrier_sync(3, 256);
+                ptx::named_barrier_sync(1 + C::WGS, C::SOFT);
                 const int c_last = walk.last_block();
                 if (tid == 0) {
                     __threadfence();
@@ -457,12 +469,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     if (last) p.tickets[c_first] = 0;
                     *bcast = last;
                 }
-                ptx::named_barrier_sync(3, 256);
+                ptx::named_barrier_sync(1 + C::WGS, C::SOFT);
                 const bool join = *bcast != 0;
-                ptx::named_barrier_sync(3, 256);  // read before the next unit's is written
+                ptx::named_barrier_sync(1 + C::WGS, C::SOFT);  // read before the next unit's is written
                 if (join) {
                     __threadfence();
-                    join_parts<D, 8, 4, 2>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
+                    join_parts<D, 4 * C::WGS, 2, 2>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
                                            walk.row0, rows_here, warp - 4, lane);
                 }
             }
