@@ -124,6 +124,12 @@ __device__ __forceinline__ EntryStream<Places> entry_stream(const int* P_dev, in
     return EntryStream<Places>(P_dev, batch, cap, units, f);
 }
 
+// One arrival for a warp whose lanes are all done (32 arrivals at one barrier queue there).
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+}
+
 // Copies rows of K and V, eight at a time, by one warp: lane l < 8 gives the rows (of VPR 16-byte vectors) that move
 // l reads and writes, -1 for none.  K and V of one row (of two, four at smaller head dims) are the warp's 32 vectors;
 // all of the eight are loaded before the first is stored.

@@ -128,9 +128,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NST; ++i) ptx::mbar_init(&k_full[i], 1), ptx::mbar_init(&k_empty[i], 1);
         for (int i = 0; i < C::QB; ++i) ptx::mbar_init(&q_full[i], 1), ptx::mbar_init(&q_empty[i], 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 128);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 4);
         ptx::mbar_init(drain, 1);
-        ptx::mbar_init(done, 256);
+        ptx::mbar_init(done, 8);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -330,11 +330,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(&s_free[g]);
+            mbar_arrive_warp(&s_free[g], lane);
             if (at >= 0) p.weight_out[at] = before + (p.pages.page(entry) >= 0 ? sum : 0.f);
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(done);
+        mbar_arrive_warp(done, lane);
     }
 }
 

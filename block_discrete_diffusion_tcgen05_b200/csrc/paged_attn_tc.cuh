@@ -104,13 +104,13 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
         ptx::mbar_init(q_empty, 1);
         for (int i = 0; i < C::NK; ++i) ptx::mbar_init(&k_full[i], 1), ptx::mbar_init(&k_empty[i], 1);
         for (int i = 0; i < C::NV; ++i) ptx::mbar_init(&v_full[i], 1), ptx::mbar_init(&v_empty[i], 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], C::SOFT);
-        ptx::mbar_init(p_full, C::SOFT);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 4 * C::WGS);
+        ptx::mbar_init(p_full, 4 * C::WGS);
         ptx::mbar_init(pv_done, 1);
-        ptx::mbar_init(o_free, C::SOFT);
+        ptx::mbar_init(o_free, 4 * C::WGS);
         ptx::mbar_init(s_drain, 1);
         ptx::mbar_init(pv_drain, 1);
-        ptx::mbar_init(done, C::SOFT);
+        ptx::mbar_init(done, 4 * C::WGS);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                     for (int j = 0; j < NH; ++j) x[j] = __uint_as_float(raw[j]);
                 }
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&s_free[sb]);  // the next S^T product may overwrite the buffer
+                mbar_arrive_warp(&s_free[sb], lane);  // the next S^T product may overwrite the buffer
                 if (!key_ok)
 #pragma unroll
                     for (int j = 0; j < NH; ++j) x[j] = -INFINITY;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(p_full);
+                mbar_arrive_warp(p_full, lane);
             }
             // ---- the unit's end: column sums over the keys, O^T out of tensor memory
             const bool whole = walk.whole;
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
             }
             if (walk.n > 0) {
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(o_free);
+                mbar_arrive_warp(o_free, lane);
             }
             if (!whole) {
                 // publish; the last block of the unit joins all of them
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
             }
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(done);
+        mbar_arrive_warp(done, lane);
     }
 }
 
