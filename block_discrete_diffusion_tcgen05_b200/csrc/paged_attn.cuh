@@ -160,18 +160,16 @@ struct StreamCut {
 };
 
 // Blocks that a call's stream is cut over: as many as keep about min_stages stages each, one per unit at least, at
-// most the grid.  Units of equal length are cut into equal parts each, if that leaves no more than a fifth of the
-// blocks idle: a block whose range meets two units joins twice.
+// most the grid.  Units of equal length are cut at their ends -- into equal parts each, or so many whole units per
+// block -- if that leaves no more than a fifth of the blocks idle: a block whose range meets the ends of two units
+// publishes and joins twice.
 __device__ __forceinline__ int paged_parts(unsigned total, unsigned units, bool equal, unsigned grid, int min_stages) {
     const unsigned want = max(total / min_stages, units);
-    if (want >= grid) {
-        if (equal && units <= grid) {
-            const unsigned aligned = grid - grid % units;
-            if (5 * aligned >= 4 * grid) return aligned;
-        }
-        return grid;
-    }
-    return equal ? want - want % units : want;
+    if (want < grid) return equal ? want - want % units : want;
+    if (!equal) return grid;
+    const unsigned per = (units + grid - 1) / grid;  // whole units per block, where there are more units than blocks
+    const unsigned aligned = units <= grid ? grid - grid % units : (units % per == 0 ? units / per : 0);
+    return 5 * aligned >= 4 * grid ? aligned : grid;
 }
 
 // Four columns of an output row from their weighted sum and the sum of the weights.
