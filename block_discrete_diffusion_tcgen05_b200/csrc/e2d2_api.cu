@@ -1025,9 +1025,13 @@ e2d2_status launch_paged_tc(const PagedAttnParams& a, const DeviceInfo* di, cuda
 
 template <int D>
 e2d2_status launch_paged_rows(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
-    if (a.rows <= 16) return launch_paged<D, 1>(a, di, stream);
-    if (a.rows <= 32) return launch_paged<D, 2>(a, di, stream);
-    return launch_paged<D, 4>(a, di, stream);
+    if constexpr (D == 128) {  // more rows: launch_paged_tc
+        return launch_paged<D, 1>(a, di, stream);
+    } else {
+        if (a.rows <= 16) return launch_paged<D, 1>(a, di, stream);
+        if (a.rows <= 32) return launch_paged<D, 2>(a, di, stream);
+        return launch_paged<D, 4>(a, di, stream);
+    }
 }
 
 template <int D, int N>

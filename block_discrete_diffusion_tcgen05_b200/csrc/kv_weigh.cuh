@@ -59,13 +59,36 @@ struct WeighCfg {
     // k_full[NST], k_empty[NST], q_full[QB], q_empty[QB], s_full[2], s_free[2], drain, done
     static constexpr int NBAR = 2 * NST + 2 * QB + 6;
     static constexpr int OFF_LSE = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // float [8 warps][N]
-    static constexpr int OFF_MISC = OFF_LSE + 8 * N * 4;                       // holder, abort
-    static constexpr int BYTES = OFF_MISC + 8;
+    static constexpr int OFF_MISC = OFF_LSE + 8 * N * 4;                       // holder, abort, plan
+    static constexpr int BYTES = OFF_MISC + 8 + 24;
     static constexpr int ALLOC = (BYTES + 1023) / 1024 * 1024 + 1024;
     static_assert(NST >= 2 && ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
 };
 
 __device__ __forceinline__ unsigned weigh_tiles(int P) { return (P + kWeighKeys - 1) / kWeighKeys; }
+
+// A block's place in the stream of tiles, worked out by one warp for all.
+struct WeighPlan {
+    unsigned left;
+    int b, h, P, t;
+};
+
+__device__ __forceinline__ void weigh_plan(const WeighParams& p, WeighPlan* out) {
+    auto stream = entry_stream(p.P_dev, p.batch, p.pages.capacity(), p.pages.kv_heads, [](int rows) { return weigh_tiles(rows); });
+    WeighPlan n;
+    const unsigned q = stream.total / gridDim.x, r = stream.total % gridDim.x, c = blockIdx.x;
+    const unsigned first = c * q + c * r / gridDim.x;
+    n.left = (c + 1) * q + (c + 1) * r / gridDim.x - first;
+    n.b = n.h = n.P = n.t = 0;
+    if (n.left > 0) {
+        unsigned before;
+        stream.find(first, n.b, before, n.P);
+        const unsigned tiles = weigh_tiles(n.P);
+        n.h = (first - before) / tiles;
+        n.t = static_cast<int>(first - before - n.h * tiles) - 1;
+    }
+    if ((threadIdx.x & 31) == 0) *out = n;
+}
 
 // Walks the tiles of this block: unit (entry b, kv head h), key tile t of it.
 struct WeighWalk {
@@ -74,19 +97,8 @@ struct WeighWalk {
     int b, h, P, tiles;
     int unit, t;     // the current tile's unit (b * Hkv + h) and index
 
-    template <class Stream>
-    __device__ WeighWalk(const WeighParams& prm, Stream stream)
-        : p(prm), b(0), h(0), P(0), tiles(0), unit(0), t(0) {
-        const unsigned q = stream.total / gridDim.x, r = stream.total % gridDim.x, c = blockIdx.x;
-        const unsigned first = c * q + c * r / gridDim.x;
-        left = (c + 1) * q + (c + 1) * r / gridDim.x - first;
-        if (left == 0) return;
-        unsigned before;
-        stream.find(first, b, before, P);
-        tiles = weigh_tiles(P);
-        h = (first - before) / tiles;
-        t = static_cast<int>(first - before - h * tiles) - 1;
-    }
+    __device__ WeighWalk(const WeighParams& prm, const WeighPlan& n)
+        : p(prm), left(n.left), b(n.b), h(n.h), P(n.P), tiles(weigh_tiles(n.P)), unit(0), t(n.t) {}
     // Moves to the next tile; false at the end.
     __device__ bool next() {
         if (left == 0) return false;
@@ -141,7 +153,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
     if (warp == 0) test_producer_delay();
     ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
     const int cap = p.pages.capacity(), Hkv = p.pages.kv_heads;
-    const auto stream = entry_stream(p.P_dev, p.batch, cap, Hkv, [](int rows) { return weigh_tiles(rows); });
+    WeighPlan* plan = reinterpret_cast<WeighPlan*>(smem + C::OFF_MISC + 8);
+    if (warp == 0) weigh_plan(p, plan);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -156,7 +169,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             ptx::tma_prefetch_desc(&p.tm_q);
         }
         const int boxes = kWeighKeys / p.box_rows;
-        WeighWalk walk(p, stream);
+        WeighWalk walk(p, *plan);
         // A tile ahead of the one being loaded: its unit, and lane's box of it (row in the page, -1 for none; the
         // table's entry, on its way).
         struct Ahead {
@@ -229,7 +242,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         const uint64_t desc = ptx::smem_desc(0, 16, 8 * C::RB, C::SWZ);  // K (A) and Q (B): K-major
         const uint32_t idesc = ptx::idesc_bf16_f32(kWeighKeys, n16, false, false);
         constexpr int KPC = C::RB / 32;  // 16-element steps per column chunk
-        WeighWalk walk(p, stream);
+        WeighWalk walk(p, *plan);
         uint32_t it = 0, units = 0;
         int have = -1;
         bool ok = true;
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         // Warpgroup g takes every other tile; every warp has its own copy of the normalisers.
         const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane;
         float* lse2 = reinterpret_cast<float*>(smem + C::OFF_LSE) + (warp - 4) * N;
-        WeighWalk walk(p, stream);
+        WeighWalk walk(p, *plan);
         // The tile ahead: its weight and its table entry are on their way while this one's scores are waited
         // for.  at < 0: no row of this thread's.
         int unit_n = -1;

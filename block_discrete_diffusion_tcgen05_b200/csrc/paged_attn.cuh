@@ -90,7 +90,8 @@ struct PagedCfg {
     static constexpr int OFF_BAD = OFF_BAR + (2 * NST + 1) * 8;   // int [NST]: groups of 16 keys that no page backs
     static constexpr int OFF_STAT = (OFF_BAD + NST * 4 + 15) / 16 * 16;  // float m[SLICES][ROWS], l[SLICES][ROWS]
     static constexpr int OFF_MISC = OFF_STAT + 2 * SLICES * ROWS * 4;    // abort, broadcast
-    static constexpr int ALLOC = OFF_MISC + 16 + 1024;      // + alignment slack
+    static constexpr int OFF_PLAN = OFF_MISC + 16;
+    static constexpr int ALLOC = OFF_PLAN + 32 + 1024;      // + alignment slack
     static_assert(NST >= 2 && CTAS * (ALLOC + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -263,9 +264,37 @@ __device__ __forceinline__ void join_parts(const PagedAttnParams& p, const float
     }
 }
 
-// The units of a block: its range of the stream, unit by unit.  KEYS: of a stage; ROWS: of a unit; MIN_KEYS: that a
-// block of a cut unit should keep.  Every thread of a warp walks alike.
-template <int KEYS, int ROWS, int MIN_KEYS>
+// A block's place in the stream, worked out by one warp for all (every warp for itself cost more in issue slots).
+struct PagedPlan {
+    unsigned lead, pos, end, ent_beg, total;
+    int parts, b, P;
+};
+
+// KEYS: of a stage; MIN_KEYS: that a block of a cut unit should keep.  One warp calls it.
+template <int KEYS, int MIN_KEYS>
+__device__ __forceinline__ void paged_plan(const PagedAttnParams& p, PagedPlan* out) {
+    const int upe = p.pages.kv_heads * p.qtiles, own = p.own ? p.S : 0;
+    auto stream = entry_stream(p.P_dev, p.batch, p.pages.capacity(), upe,
+                               [own](int rows) { return static_cast<unsigned>(max(1, paged_stages(rows, own, KEYS))); });
+    PagedPlan n;
+    n.lead = stream.equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
+    stream.lead = n.lead;
+    n.total = stream.total + n.lead * p.batch * upe;
+    n.parts = paged_parts(n.total, p.batch * upe, stream.equal, gridDim.x, MIN_KEYS / KEYS);
+    n.pos = n.end = n.ent_beg = 0;
+    n.b = n.P = 0;
+    if (static_cast<int>(blockIdx.x) < n.parts) {
+        const StreamCut cut(n.total, n.parts);
+        n.pos = cut.begin(blockIdx.x);
+        n.end = cut.begin(blockIdx.x + 1);
+        stream.find(n.pos, n.b, n.ent_beg, n.P);
+    }
+    if ((threadIdx.x & 31) == 0) *out = n;
+}
+
+// The units of a block: its range of the stream, unit by unit.  ROWS: query rows of a unit.  Every thread of a warp
+// walks alike.
+template <int KEYS, int ROWS>
 struct PagedWalk {
     const PagedAttnParams& p;
     int upe, own_rows, n_own;     // units per entry; the own block's rows and stages
@@ -277,23 +306,11 @@ struct PagedWalk {
     unsigned ubeg, len;           // its first place in the stream, its places
     bool whole;                   // all of it is this block's
 
-    __device__ explicit PagedWalk(const PagedAttnParams& prm) : p(prm), pos(0), end(0) {
-        const int Hkv = p.pages.kv_heads;
-        upe = Hkv * p.qtiles;
+    __device__ PagedWalk(const PagedAttnParams& prm, const PagedPlan& n)
+        : p(prm), lead(n.lead), pos(n.pos), end(n.end), ent_beg(n.ent_beg), total(n.total), parts(n.parts), next_b(n.b), next_P(n.P) {
+        upe = p.pages.kv_heads * p.qtiles;
         own_rows = p.own ? p.S : 0;
         n_own = (own_rows + KEYS - 1) / KEYS;
-        const int own = own_rows;
-        auto stream = entry_stream(p.P_dev, p.batch, p.pages.capacity(), upe,
-                                   [own](int rows) { return static_cast<unsigned>(max(1, paged_stages(rows, own, KEYS))); });
-        lead = stream.equal ? 0 : kPagedUnitStages;  // empty places ahead of a unit's stages
-        stream.lead = lead;
-        total = stream.total + lead * p.batch * upe;
-        parts = paged_parts(total, p.batch * upe, stream.equal, gridDim.x, MIN_KEYS / KEYS);
-        if (idle()) return;
-        const StreamCut cut(total, parts);
-        pos = cut.begin(blockIdx.x);
-        end = cut.begin(blockIdx.x + 1);
-        stream.find(pos, next_b, ent_beg, next_P);
     }
     __device__ bool idle() const { return static_cast<int>(blockIdx.x) >= parts; }
     __device__ bool next() {
@@ -372,9 +389,11 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     if (loads) test_producer_delay();
     ptx::griddep_wait();  // lengths, table and rows are read after the previous kernel on the stream
 
-    PagedWalk<KEYS, ROWS, kPagedMinKeys> walk(p);
+    PagedPlan* plan = reinterpret_cast<PagedPlan*>(smem + C::OFF_PLAN);
+    if (loads) paged_plan<KEYS, kPagedMinKeys>(p, plan);
+    __syncthreads();  // the barriers are initialised, the plan is written
+    PagedWalk<KEYS, ROWS> walk(p, *plan);
     if (walk.idle()) return;
-    __syncthreads();  // the barriers are initialised
 
     const int rw = warp % RW, slice = warp / RW;
     const uint32_t ring = ptx::smem_u32(smem + C::OFF_RING);

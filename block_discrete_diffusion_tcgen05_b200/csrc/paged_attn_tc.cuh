@@ -55,7 +55,9 @@ struct TcCfg {
     static constexpr int OFF_CMAX = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // float [WGS][2 parity][4 warps][NH]
     static constexpr int OFF_LRED = OFF_CMAX + WGS * 2 * 4 * NH * 4;      // float [WGS][4 warps][NH]
     static constexpr int OFF_MISC = OFF_LRED + WGS * 4 * NH * 4;          // holder, abort, broadcast
-    static constexpr int ALLOC = OFF_MISC + 16 + 1024;                    // + alignment slack
+    static constexpr int OFF_PLAN = OFF_MISC + 16;
+    static constexpr int OFF_INV = OFF_PLAN + 32;                         // float [N]: 1 / sum of a column
+    static constexpr int ALLOC = OFF_INV + N * 4 + 1024;                  // + alignment slack
     static_assert(ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
 };
 
@@ -127,12 +129,14 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
         test_producer_delay();
     }
     ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
+    PagedPlan* plan = reinterpret_cast<PagedPlan*>(smem + C::OFF_PLAN);
+    if (warp == 0) paged_plan<kTcKeys, kTcMinKeys>(p, plan);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
     const int Hkv = p.pages.kv_heads;
-    PagedWalk<kTcKeys, N, kTcMinKeys> walk(p);  // an idle block's has no units: its roles fall through
+    PagedWalk<kTcKeys, N> walk(p, *plan);  // an idle block's has no units: its roles fall through
     // rows of tile c of the unit at hand, and whether it is the own block's
     auto tile_rows = [&](int c, bool& is_own) {
         is_own = c < walk.n_own;
@@ -415,13 +419,37 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
             const int rows_here = walk.rows_here;
             const int c_first = whole ? 0 : walk.first_block();
             float* slot = whole ? nullptr : walk.slot(blockIdx.x, c_first);
+            float* inv_l = reinterpret_cast<float*>(smem + C::OFF_INV) + g * NH;
             if (walk.n > 0) {
                 const float mine = warp_columns_reduce<NH>(l_part, lane, [](float a, float b) { return a + b; });
                 if ((lane % (32 / NH)) == 0) lred[w * NH + lane / (32 / NH)] = mine;
                 ptx::named_barrier_sync(1 + g, 128);
+            }
+            if (w == 0 && lane < NH) {
+                // lane = column: its sum, maximum, normaliser
+                const float l = walk.n > 0 ? (lred[lane] + lred[NH + lane]) + (lred[2 * NH + lane] + lred[3 * NH + lane]) : 0.f;
+                float nm = neg_m[0];
+#pragma unroll
+                for (int j = 1; j < NH; ++j) nm = lane == j ? neg_m[j] : nm;
+                const int col = g * NH + lane;
+                if (whole) {
+                    // (a unit without keys writes zeros and leaves the last unit's values to their readers)
+                    if (walk.n > 0) inv_l[lane] = l > 0.f ? 1.f / l : 0.f;
+                    if (p.lse != nullptr && col < rows_here)
+                        p.lse[walk.row0 + col] = l > 0.f ? (log2f(l) - nm) * 0.69314718055994531f : -INFINITY;
+                } else if (col < rows_here) {
+                    __stcg(slot + p.rows_cap * D + col, l > 0.f ? -nm : -INFINITY);
+                    __stcg(slot + p.rows_cap * D + p.rows_cap + col, l);
+                }
+            }
+            if (walk.n > 0) {
                 wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
                 ptx::tc_fence_after();
             }
+            if (whole) ptx::named_barrier_sync(1 + g, 128);  // inv_l is written
+            const int cols = min(NH, rows_here - g * NH);    // rows of this warpgroup's columns
+            __nv_bfloat16* out = p.out + (walk.row0 + g * NH) * D + key;
+            float* part = whole ? nullptr : slot + g * NH * D + key;
 #pragma unroll
             for (int c8 = 0; c8 < NH; c8 += 8) {
                 uint32_t oh[8], ol[8];
@@ -437,20 +465,11 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int j = c8 + k, col = g * NH + j;
-                    if (col >= rows_here) continue;
                     const float o = __uint_as_float(oh[k]) + __uint_as_float(ol[k]);
-                    const float l = walk.n > 0 ? (lred[j] + lred[NH + j]) + (lred[2 * NH + j] + lred[3 * NH + j]) : 0.f;
                     if (whole) {
-                        p.out[(walk.row0 + col) * D + key] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-                        if (key == 0 && p.lse != nullptr)
-                            p.lse[walk.row0 + col] = l > 0.f ? (log2f(l) - neg_m[j]) * 0.69314718055994531f : -INFINITY;
-                    } else {
-                        __stcg(slot + col * D + key, o);
-                        if (key == 0) {
-                            __stcg(slot + p.rows_cap * D + col, l > 0.f ? -neg_m[j] : -INFINITY);
-                            __stcg(slot + p.rows_cap * D + p.rows_cap + col, l);
-                        }
+                        if (c8 + k < cols) out[(c8 + k) * D] = __float2bfloat16_rn(walk.n > 0 ? o * inv_l[c8 + k] : 0.f);
+                    } else if (c8 + k < cols) {
+                        __stcg(part + (c8 + k) * D, o);
                     }
                 }
             }
@@ -474,7 +493,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 ptx::named_barrier_sync(1 + C::WGS, C::SOFT);  // read before the next unit's is written
                 if (join) {
                     __threadfence();
-                    join_parts<D, 4 * C::WGS, 2, 2>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
+                    join_parts<D, 4 * C::WGS, 2, 4>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
                                            walk.row0, rows_here, warp - 4, lane);
                 }
             }
