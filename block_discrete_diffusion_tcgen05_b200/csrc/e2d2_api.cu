@@ -992,15 +992,13 @@ int box_of(const e2d2_pages& pages, int most) {
     return box;
 }
 
-// bf16 tensor [units][rows][D] whose boxes hold every column of box_rows rows: 4D, the row's column halves of 128
-// bytes (one, of all columns, at D <= 64) as a dimension, so that one copy fills both swizzled halves.
-bool map_rows(CUtensorMap* m, const void* base, int D, long long rows, long long units, int box_rows) {
+// bf16 rows [rows][D] whose boxes hold every column of box_rows rows: the row's column halves of 128 bytes (one, of all
+// columns, at D <= 64) are a dimension, so that one copy fills the swizzled halves one after the other.
+bool map_queries(CUtensorMap* m, const void* base, int D, long long rows, int box_rows) {
     const int rb = (D * 2 < 128) ? D * 2 : 128;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(rb / 2), static_cast<cuuint64_t>(rows),
-                          static_cast<cuuint64_t>(D * 2 / rb), static_cast<cuuint64_t>(units)};
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(rb / 2), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(D * 2 / rb), 1};
     cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rb), static_cast<cuuint64_t>(rows) * D * 2};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(rb / 2), static_cast<cuuint32_t>(box_rows),
-                         static_cast<cuuint32_t>(D * 2 / rb), 1};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(rb / 2), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(D * 2 / rb), 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -1025,13 +1023,9 @@ e2d2_status launch_paged_tc(const PagedAttnParams& a, const DeviceInfo* di, cuda
 
 template <int D>
 e2d2_status launch_paged_rows(const PagedAttnParams& a, const DeviceInfo* di, cudaStream_t stream) {
-    if constexpr (D == 128) {  // more rows: launch_paged_tc
-        return launch_paged<D, 1>(a, di, stream);
-    } else {
-        if (a.rows <= 16) return launch_paged<D, 1>(a, di, stream);
-        if (a.rows <= 32) return launch_paged<D, 2>(a, di, stream);
-        return launch_paged<D, 4>(a, di, stream);
-    }
+    if (a.rows <= 16) return launch_paged<D, 1>(a, di, stream);
+    if (a.rows <= 32) return launch_paged<D, 2>(a, di, stream);
+    return launch_paged<D, 4>(a, di, stream);
 }
 
 template <int D, int N>
@@ -1148,21 +1142,17 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     PagedAttnParams a;
     const long long units = static_cast<long long>(pages.num_pages) * dims.kv_heads;
     a.rows = dims.q_heads / dims.kv_heads * S;
-    const bool tc = D == 128 && a.rows > kPagedTcRows;  // tensor-memory kernel
+    const bool tc = D == 128;  // the tensor-memory kernel's lanes are keys and head dims
     const int rw = a.rows <= 16 ? 1 : (a.rows <= 32 ? 2 : 4);
-    const int keys = tc ? kTcKeys : (D == 128 ? 64 : 128) / rw;  // of a stage
+    const int keys = tc ? kTcKeys : 128 / rw;  // of a stage
     a.box_rows = box_of(pages, keys);
     a.own_box = 16;
     while (a.own_box < S && a.own_box < keys) a.own_box *= 2;
-    bool ok = map_rows(&a.tm_q, q_blk, D, static_cast<long long>(dims.batch) * dims.q_heads * S, 1, 16 * rw);
-    if (tc)
-        ok = ok && map_3d(&a.tm_k, k_pages, D, pages.page_rows, units, pages.page_rows, a.box_rows) &&
-             map_3d(&a.tm_v, v_pages, D, pages.page_rows, units, pages.page_rows, a.box_rows) &&
-             (!k_blk || (map_3d(&a.tm_k1, k_blk, D, S, BHkv, S, a.own_box) && map_3d(&a.tm_v1, v_blk, D, S, BHkv, S, a.own_box)));
-    else
-        ok = ok && map_rows(&a.tm_k, k_pages, D, pages.page_rows, units, a.box_rows) &&
-             map_rows(&a.tm_v, v_pages, D, pages.page_rows, units, a.box_rows) &&
-             (!k_blk || (map_rows(&a.tm_k1, k_blk, D, S, BHkv, a.own_box) && map_rows(&a.tm_v1, v_blk, D, S, BHkv, a.own_box)));
+    bool ok = map_queries(&a.tm_q, q_blk, D, static_cast<long long>(dims.batch) * dims.q_heads * S, 16 * rw) &&
+              map_3d(&a.tm_k, k_pages, D, pages.page_rows, units, pages.page_rows, a.box_rows) &&
+              map_3d(&a.tm_v, v_pages, D, pages.page_rows, units, pages.page_rows, a.box_rows);
+    if (ok && k_blk)
+        ok = map_3d(&a.tm_k1, k_blk, D, S, BHkv, S, a.own_box) && map_3d(&a.tm_v1, v_blk, D, S, BHkv, S, a.own_box);
     if (!ok) return E2D2_ERR_CUDA;
     if (!k_blk) a.tm_k1 = a.tm_k, a.tm_v1 = a.tm_v;
     a.pages = page_view(pages, dims, di);
@@ -1181,12 +1171,13 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
     a.rows_cap = w.rows_cap;
     a.slot_floats = w.slot_floats;
     a.scale_log2 = scale_log2(dims);
-    if (tc) return a.rows <= 32 ? launch_paged_tc<32>(a, di, stream) : launch_paged_tc<64>(a, di, stream);
     switch (D) {
         case 32: return launch_paged_rows<32>(a, di, stream);
         case 64: return launch_paged_rows<64>(a, di, stream);
-        default: return launch_paged_rows<128>(a, di, stream);
+        default: break;
     }
+    if (a.rows <= 16) return launch_paged_tc<16>(a, di, stream);
+    return a.rows <= 32 ? launch_paged_tc<32>(a, di, stream) : launch_paged_tc<64>(a, di, stream);
 }
 
 e2d2_status e2d2_kv_cache_append_paged(void* k_pages, void* v_pages, e2d2_pages pages, const int* P_dev,

@@ -1,4 +1,5 @@
-// paged_attn.cuh -- the sampling step over a paged KV cache.
+// paged_attn.cuh -- the sampling step over a paged KV cache: the cut of the work over blocks and the join of their
+// parts, for every head size, and the kernel for head sizes 32 and 64 (128: paged_attn_tc.cuh).
 //
 //   x_ij = scale q_i . k_j,  lse_i = log sum_j exp(x_ij),  out_i = sum_j exp(x_ij - lse_i) v_j
 //
@@ -9,17 +10,18 @@
 // rows are more units), so a call is bound by HBM until some 64 rows share a head.  Everything is arranged for
 // bytes in flight.  A block is one warp that loads and four that compute; three blocks share an SM, so one streams
 // while another starts or joins.  The loader fills a ring of stages, K and V, in boxes of as many rows as pages
-// allow (16 at least: a page of any multiple of 16 rows is a whole number of boxes), both column halves of a row in
-// one copy -- issuing copies is what bounds a loader, about a hundred clocks each -- and its lanes look up the
-// pages of the next stages ahead of time.  A consumer warp takes 16 keys (32 at d <= 64) of every stage and 16
-// query rows, and runs the online softmax of its own keys with its own running maximum, without a word to the
+// allow (16 at least: a page of any multiple of 16 rows is a whole number of boxes; issuing copies is what bounds a
+// loader, about a hundred clocks each), and its lanes look up the pages of the next stages ahead of time.  A
+// consumer warp takes 32 keys of every stage and 16 query rows, and runs the online softmax of its own keys with its own running maximum, without a word to the
 // others before the unit ends.
 //
-// The products use mma.sync with the query rows on the 16-row side: with 1 to 32 rows a tensor-memory
-// accumulator would be almost empty, and the scores would have to travel TMEM -> registers -> shared memory
-// between the two products, where here they stay in the registers that the first product leaves them in.  The
-// probabilities enter the second product as the sum of two bf16 (value and remainder): held to 16 bits and
-// more, they add nothing to the rounding of the output, for tensor-core time that the loads hide.
+// The products use mma.sync with the query rows on the 16-row side: head sizes 32 and 64 do not fill the 128 lanes that
+// V^T P^T takes in tensor memory, and the scores stay in the registers that the first product leaves them in, where
+// the second one wants them.  The probabilities enter the second product as the sum of two bf16 (value and remainder):
+// held to 16 bits and more, they add nothing to the rounding of the output, for tensor-core time that the loads hide.
+// At d = 128 this kernel took 92.9 us for 32 single tokens over up to 8192 rows (89 % of the copy rate) against 95.2 us
+// of the tensor-memory kernel, but 11.8 against 9.5 us for one token over 500 rows, and 68 against 52 us and 198
+// against 109 us for blocks of 32 and 64 query rows.
 //
 // The stages of all units form one stream that is cut evenly over the blocks (lengths are read on the device,
 // so any mix of lengths is balanced); where lengths differ a unit takes kPagedUnitStages empty places ahead of its
@@ -42,9 +44,9 @@ constexpr int kPagedUnitStages = 4; // what beginning and joining a unit costs, 
 constexpr int kPagedMinKeys = 256;  // keys per block that the split aims for
 
 struct alignas(64) PagedAttnParams {
-    CUtensorMap tm_k, tm_v;    // pools: 4D {D half, page_rows, halves, num_pages * Hkv}, boxes of box_rows
-    CUtensorMap tm_k1, tm_v1;  // own block, the same over {.., S, .., B * Hkv}, boxes of own_box
-    CUtensorMap tm_q;          // queries: the same over {.., B * Hq * S, .., 1}, boxes of a unit's rows
+    CUtensorMap tm_k, tm_v;    // pools: 3D {D, page_rows, num_pages * Hkv}, boxes of box_rows
+    CUtensorMap tm_k1, tm_v1;  // own block: 3D {D, S, B * Hkv}, boxes of own_box
+    CUtensorMap tm_q;          // queries: rows of [B * Hq * S][D], every column of a unit's rows in a box
     PageView pages;
     const int* P_dev;
     __nv_bfloat16* out;        // [B][Hq][S][D]
@@ -67,21 +69,21 @@ struct alignas(64) PagedAttnParams {
 template <int D_, int RW_>
 struct PagedCfg {
     static constexpr int D = D_, RW = RW_;
+    static_assert(D == 32 || D == 64, "one column chunk per row");
     static constexpr int CTAS = 3;                          // blocks per SM
     static constexpr int WARPS = 4;                         // consumer warps
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int SLICES = WARPS / RW;
     static constexpr int ROWS = 16 * RW;                    // query rows of a unit
-    static constexpr int SK = D == 128 ? 16 : 32;           // keys of a slice
+    static constexpr int SK = 32;                           // keys of a slice
     static constexpr int SUB = SK / 16;
     static constexpr int KEYS = SK * SLICES;                // keys of a stage
-    static constexpr int RB = D * 2 < 128 ? D * 2 : 128;    // bytes per row of one column half
-    static constexpr int NCH = D * 2 / RB;                  // column halves (1 at d <= 64)
-    static constexpr int KB = KEYS * D * 2;
+    static constexpr int RB = D * 2;                        // bytes per row
+    static constexpr int KB = KEYS * RB;
     static constexpr int STAGE = 2 * KB;
     static constexpr int RING = (RW <= 2 ? 64 : 48) * 1024;
     static constexpr int NST = RING / STAGE;
-    static constexpr int QCHUNK = ROWS * RB, Q_BYTES = NCH * QCHUNK;
+    static constexpr int Q_BYTES = ROWS * RB;
     static constexpr int RSTRIDE = D + 8;                   // floats per row of the join buffer (in the ring)
     static_assert(SLICES * ROWS * RSTRIDE * 4 <= RING, "the ring holds the join");
     static constexpr int OFF_RING = 0;
@@ -95,12 +97,12 @@ struct PagedCfg {
     static_assert(NST >= 2 && CTAS * (ALLOC + 1024) <= 228 * 1024, "shared memory");
 };
 
-// All columns of `rows` (the box's) rows from row y of pool index z.
-__device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint64_t* bar, void* dst, int y, int z) {
+// A box of query rows from row y on, all columns (the row's halves of 128 bytes are a dimension of the map).
+__device__ __forceinline__ void tma_load_q(const CUtensorMap* map, uint64_t* bar, void* dst, int y) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %3, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(y), "r"(z)
+        " [%0], [%1, {%3, %4, %3, %3}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(y)
         : "memory");
 }
 
@@ -125,13 +127,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte offset of 16-byte unit u of row r in a tile of column halves of `half` bytes (rows of D bf16), as the
-// swizzled TMA boxes leave it.
+// Byte offset of 16-byte unit u of row r in a tile of rows of D bf16, as the swizzled TMA boxes leave it.
 template <int D>
-__device__ __forceinline__ uint32_t tile_offset(int r, int u, int half) {
-    constexpr int RB = D * 2 < 128 ? D * 2 : 128, UPC = RB / 16;
-    const int x = RB == 128 ? (r & 7) : ((r >> 1) & 3);
-    return static_cast<uint32_t>((u / UPC) * half + r * RB + (((u % UPC) ^ x) << 4));
+__device__ __forceinline__ uint32_t tile_offset(int r, int u) {
+    const int x = D == 64 ? (r & 7) : ((r >> 1) & 3);
+    return static_cast<uint32_t>(r * D * 2 + ((u ^ x) << 4));
 }
 
 // Stages of a unit's keys: the own block's, then the cached rows'.
@@ -399,18 +399,12 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     const uint32_t ring = ptx::smem_u32(smem + C::OFF_RING);
     const int g8 = lane >> 2, t4 = lane & 3;
     // ldmatrix lane addresses: matrix lane / 8, row lane % 8.  K: keys 0-7, 8-15 of two 16-byte units; V
-    // (transposed) and Q: rows 0-7, 8-15 of one unit, then of the next.  The swizzle depends on the lane alone;
-    // step j (two units) is an XOR of 32 j inside a column half.
-    const int l7 = lane & 7, mat = lane >> 3;
-    const uint32_t ok_ = tile_offset<D>(l7 + (mat >> 1) * 8, mat & 1, 0);
-    const uint32_t ov_ = tile_offset<D>(l7 + (mat & 1) * 8, mat >> 1, 0);
-    const uint32_t oq_ = ptx::smem_u32(smem + C::OFF_Q) + tile_offset<D>(rw * 16 + l7 + (mat & 1) * 8, mat >> 1, 0);
-    // A stage lies in shared memory box by box, [box][column half][row]: this warp's slice of it, and the distance
-    // of the halves.
-    const int key0 = slice * SK;
-    auto slice_base = [&](int box) { return static_cast<uint32_t>(key0 / box * (box * D * 2) + key0 % box * C::RB); };
-    const uint32_t base_pool = slice_base(p.box_rows), base_own = slice_base(p.own_box);
-    constexpr int SPC = C::RB / 32;  // steps per column chunk
+    // (transposed) and Q: rows 0-7, 8-15 of one unit, then of the next.  The swizzle depends on the lane alone; step j
+    // (two units) is an XOR of 32 j.
+    const int l7 = lane & 7, mat = lane >> 3, key0 = slice * SK;
+    const uint32_t ok_ = tile_offset<D>(key0 + l7 + (mat >> 1) * 8, mat & 1);
+    const uint32_t ov_ = tile_offset<D>(key0 + l7 + (mat & 1) * 8, mat >> 1);
+    const uint32_t oq_ = ptx::smem_u32(smem + C::OFF_Q) + tile_offset<D>(rw * 16 + l7 + (mat & 1) * 8, mat >> 1);
     uint32_t it = 0, n_units = 0;    // stages that went through the ring so far, units
 
     const int Hkv = p.pages.kv_heads;
@@ -426,7 +420,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
             // unit's last are other units' (or zeros): no row's result depends on another row.
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(q_full, C::Q_BYTES);
-                tma_load_4d(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(row0), 0);
+                tma_load_q(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(row0));
             }
             __syncwarp();
             // A batch of 32 look-ups, NB of each stage: cur covers the stages being issued, nxt those after, loaded
@@ -478,9 +472,9 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 }
                 __syncwarp();
                 if (mine) {
-                    uint8_t* dst = smem + C::OFF_RING + st * C::STAGE + lane * box * D * 2;
-                    tma_load_4d(is_own ? &p.tm_k1 : &p.tm_k, &full[st], dst, y, z);
-                    tma_load_4d(is_own ? &p.tm_v1 : &p.tm_v, &full[st], dst + C::KB, y, z);
+                    uint8_t* dst = smem + C::OFF_RING + st * C::STAGE + lane * box * C::RB;
+                    ptx::tma_load_3d(is_own ? &p.tm_k1 : &p.tm_k, &full[st], dst, 0, y, z);
+                    ptx::tma_load_3d(is_own ? &p.tm_v1 : &p.tm_v, &full[st], dst + C::KB, 0, y, z);
                 }
                 __syncwarp();
                 if (++st == NST) st = 0, ++use;
@@ -506,9 +500,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 const int valid = (is_own ? own_rows - c * KEYS : unit_P - (c - n_own) * KEYS) - key0;
                 const int lost = (bad[st] >> (slice * SUB)) & ((1 << SUB) - 1);
                 if (valid > 0) {
-                    const int half = (is_own ? p.own_box : p.box_rows) * C::RB;
-                    const uint32_t sk = ring + st * C::STAGE + (is_own ? base_own : base_pool) + ok_;
-                    const uint32_t sv = ring + st * C::STAGE + C::KB + (is_own ? base_own : base_pool) + ov_;
+                    const uint32_t sk = ring + st * C::STAGE + ok_, sv = ring + st * C::STAGE + C::KB + ov_;
                     // S = Q K^T, even and odd steps in accumulators of their own (shorter chains)
                     float s[2 * SUB][4], s1[2 * SUB][4];
 #pragma unroll
@@ -518,11 +510,11 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         uint32_t qa[4];
-                        ldsm4((oq_ ^ ((ks % SPC) * 32)) + (ks / SPC) * C::QCHUNK, qa);
+                        ldsm4(oq_ ^ (ks * 32), qa);
 #pragma unroll
                         for (int sb = 0; sb < SUB; ++sb) {
                             uint32_t kb[4];
-                            ldsm4((sk ^ ((ks % SPC) * 32)) + (ks / SPC) * half + sb * 16 * C::RB, kb);
+                            ldsm4((sk ^ (ks * 32)) + sb * 16 * C::RB, kb);
                             mma_16816((ks & 1) ? s1[2 * sb] : s[2 * sb], qa, kb[0], kb[1]);
                             mma_16816((ks & 1) ? s1[2 * sb + 1] : s[2 * sb + 1], qa, kb[2], kb[3]);
                         }
@@ -539,10 +531,10 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (x * 8 + 2 * t4 + (e & 1) >= valid || ((lost >> (x / 2)) & 1)) s[x][e] = -INFINITY;
-                        uint8_t* v0 = smem + C::OFF_RING + st * C::STAGE + C::KB + (is_own ? base_own : base_pool);
+                        uint8_t* v0 = smem + C::OFF_RING + st * C::STAGE + C::KB;
                         for (int x = lane; x < SK * (D / 8); x += 32) {
                             const int key = x / (D / 8), u = x % (D / 8);
-                            if (key >= valid) *reinterpret_cast<uint4*>(v0 + tile_offset<D>(key, u, half)) = make_uint4(0u, 0u, 0u, 0u);
+                            if (key >= valid) *reinterpret_cast<uint4*>(v0 + tile_offset<D>(key0 + key, u)) = make_uint4(0u, 0u, 0u, 0u);
                         }
                         ptx::fence_proxy_async_smem();  // before the stage is loaded again
                         __syncwarp();
@@ -593,8 +585,8 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
 #pragma unroll
                         for (int j = 0; j < D / 16; j += 2) {
                             uint32_t v0[4], v1[4];
-                            ldsm4t((sv ^ ((j % SPC) * 32)) + (j / SPC) * half + sb * 16 * C::RB, v0);
-                            ldsm4t((sv ^ (((j + 1) % SPC) * 32)) + ((j + 1) / SPC) * half + sb * 16 * C::RB, v1);
+                            ldsm4t((sv ^ (j * 32)) + sb * 16 * C::RB, v0);
+                            ldsm4t((sv ^ ((j + 1) * 32)) + sb * 16 * C::RB, v1);
                             mma_16816(o[2 * j], ph[sb], v0[0], v0[1]);
                             mma_16816(o[2 * j + 1], ph[sb], v0[2], v0[3]);
                             mma_16816(o[2 * j + 2], ph[sb], v1[0], v1[1]);

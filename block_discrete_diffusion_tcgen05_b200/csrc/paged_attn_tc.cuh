@@ -1,5 +1,4 @@
-// paged_attn_tc.cuh -- the paged sampling step for blocks of many query rows (17 to 64 share a kv head) at d = 128, on
-// the 5th-generation tensor cores.
+// paged_attn_tc.cuh -- the paged sampling step at d = 128, on the 5th-generation tensor cores.
 //
 // As paged_attn.cuh, but with the products taken transposed and their accumulators in tensor memory:
 //
@@ -7,9 +6,8 @@
 //     O^T += V^T [P^T | R^T] M = d = 128 (lanes),   2 N columns = probabilities, remainders, K = keys
 //
 // P and R are the two bf16 that hold a probability to 16 bits and more: the remainders are N more columns of the same
-// product, added to the others' when the unit ends.  With mma.sync the rows' accumulators fill the registers from 32
-// rows on and few warps are left to hide its latencies; here a tile's softmax is that of 128 threads for every
-// 16 columns (thread = key) and the tensor cores work beside it.
+// product, added to the others' when the unit ends.  A tile's softmax is that of 128 threads for every 16 columns
+// (thread = key) and the tensor cores work beside it.  HBM bounds it at every row count.
 //
 // A column's running maximum is shared by its warpgroup's 128 keys: each tile the threads vote whether any key beats
 // any of their columns' by more than 2^8, and only then are they reduced and O^T rescaled.  It is held negated and in
@@ -28,7 +26,6 @@
 namespace e2d2 {
 
 constexpr int kTcKeys = 128;      // keys of a tile
-constexpr int kPagedTcRows = 16;  // query rows per kv head above which this kernel is taken (at d = 128)
 constexpr int kTcMinKeys = 384;   // keys per block that the split aims for
 
 template <int N_>
@@ -40,9 +37,9 @@ struct TcCfg {
     static constexpr int KV = kTcKeys * D * 2;        // K (or V) of a tile: two column halves of 128-byte rows
     static constexpr int HALF = kTcKeys * 128;
     static constexpr int Q_BYTES = N * D * 2;
-    static constexpr int P_CHUNKS = 2 * N / 64;       // 64-column chunks of [P^T | R^T]
+    static constexpr int P_CHUNKS = (2 * N + 63) / 64;  // 64-column chunks of [P^T | R^T]
     static constexpr int P_BYTES = P_CHUNKS * HALF;
-    static constexpr int NK = N == 64 ? 2 : 3, NV = 3;
+    static constexpr int NK = N == 64 ? 2 : 3, NV = 3;  // ring stages
     static constexpr uint32_t TMEM_COLS = 4 * N;      // S^T at 0 and N, O^T at 2 N
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
@@ -159,7 +156,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 if (!ok) break;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(q_full, C::Q_BYTES);
-                    tma_load_4d(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(walk.row0), 0);
+                    tma_load_q(&p.tm_q, q_full, smem + C::OFF_Q, static_cast<int>(walk.row0));
                 }
                 __syncwarp();
             }
