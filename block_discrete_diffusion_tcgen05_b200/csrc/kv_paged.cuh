@@ -124,6 +124,11 @@ __device__ __forceinline__ EntryStream<Places> entry_stream(const int* P_dev, in
     return EntryStream<Places>(P_dev, batch, cap, units, f);
 }
 
+// The test hook's delay, read while the previous kernel still runs; the producer sleeps before its first load.
+__device__ __forceinline__ bool producer_delay_set() {
+    return *reinterpret_cast<volatile unsigned long long*>(&g_test_producer_delay_ns) != 0;
+}
+
 // One arrival for a warp whose lanes are all done (32 arrivals at one barrier queue there).
 __device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
         ptx::tmem_alloc(holder, C::TMEM_COLS);
         ptx::tmem_relinquish();
     }
-    if (warp == 0) test_producer_delay();
+    const bool delayed = warp == 0 && producer_delay_set();
     ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
     const int cap = p.pages.capacity(), Hkv = p.pages.kv_heads;
     WeighPlan* plan = reinterpret_cast<WeighPlan*>(smem + C::OFF_MISC + 8);
@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid
             ptx::tma_prefetch_desc(&p.tm_k);
             ptx::tma_prefetch_desc(&p.tm_q);
         }
+        if (delayed) test_producer_delay();
         const int boxes = kWeighKeys / p.box_rows;
         WeighWalk walk(p, *plan);
         // A tile ahead of the one being loaded: its unit, and lane's box of it (row in the page, -1 for none; the

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
         ptx::tma_prefetch_desc(&p.tm_k);
         ptx::tma_prefetch_desc(&p.tm_v);
     }
-    if (loads) test_producer_delay();
+    const bool delayed = loads && producer_delay_set();
     ptx::griddep_wait();  // lengths, table and rows are read after the previous kernel on the stream
 
     PagedPlan* plan = reinterpret_cast<PagedPlan*>(smem + C::OFF_PLAN);
@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
     __syncthreads();  // the barriers are initialised, the plan is written
     PagedWalk<KEYS, ROWS> walk(p, *plan);
     if (walk.idle()) return;
+    if (delayed) test_producer_delay();
 
     const int rw = warp % RW, slice = warp / RW;
     const uint32_t ring = ptx::smem_u32(smem + C::OFF_RING);

@@ -117,13 +117,14 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
         ptx::tmem_alloc(holder, C::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    bool delayed = false;
     if (warp == 0 || warp == 2) {
         if (lane == 0) {
             ptx::tma_prefetch_desc(warp == 0 ? &p.tm_k : &p.tm_v);
             ptx::tma_prefetch_desc(warp == 0 ? &p.tm_k1 : &p.tm_v1);
             if (warp == 0) ptx::tma_prefetch_desc(&p.tm_q);
         }
-        test_producer_delay();
+        delayed = producer_delay_set();
     }
     ptx::griddep_wait();  // inputs are read after the previous kernel on the stream has finished
     PagedPlan* plan = reinterpret_cast<PagedPlan*>(smem + C::OFF_PLAN);
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
 
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- loads: warp 0 Q and K, warp 2 V
+        if (delayed) test_producer_delay();
         const bool is_k = warp == 0;
         const int NS = is_k ? C::NK : C::NV;
         uint64_t* full = is_k ? k_full : v_full;

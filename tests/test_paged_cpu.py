@@ -80,6 +80,8 @@ def test_common_refusals(lib, name, args, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), INVALID), (dict(v=None), INVALID), (dict(out=None), INVALID), (dict(kb=None), INVALID),
+    # more places in the work stream than 31 bits count
+    (dict(dims=_lib.Dims(1024, 64, 32, 64, 0.0), pages=_lib.Pages(9, 1 << 15, 1 << 6, P16), S=1), SHAPE),
     (dict(vb=None), INVALID), (dict(S=0), INVALID), (dict(S=-3), INVALID), (dict(S=1 << 28), SHAPE),
     (dict(q=MIS), ALIGNMENT), (dict(v=MIS), ALIGNMENT), (dict(kb=MIS), ALIGNMENT), (dict(vb=MIS), ALIGNMENT),
     (dict(out=MIS), ALIGNMENT), (dict(lse=P16 + 2), ALIGNMENT), (dict(ws=None), WORKSPACE), (dict(n=16), WORKSPACE),

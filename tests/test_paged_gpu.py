@@ -6,12 +6,12 @@ import numpy as np
 import pytest
 import torch
 
-from block_discrete_diffusion_tcgen05_b200 import attn
+from block_discrete_diffusion_tcgen05_b200 import _lib, attn
 import paged_reference as R
 
 pytestmark = pytest.mark.gpu
 
-E2D2_ERR_PAGE = 10
+E2D2_ERR_TIMEOUT, E2D2_ERR_PAGE = 8, 10
 
 
 def guarded(shape, dtype, fill):
@@ -71,6 +71,12 @@ CASES = [
     (3, 12, 4, 7, 64, 0, False, [37, 613, 1]),
     (2, 8, 2, 16, 32, 0, True, [613, 600]),
     (70, 4, 2, 1, 64, 16, True, [(17 * i) % 97 for i in range(70)]),
+    (45, 4, 2, 1, 128, 16, False, [(23 * i) % 301 for i in range(45)]),
+    (2, 2, 2, 150, 128, 64, True, [200, 0]),                 # a long block: its own rows take two tiles
+    (1, 2, 2, 150, 64, 16, True, [70]),
+    (3, 8, 8, 1, 128, 128, True, [512, 512, 512]),           # equal lengths: whole units, or equal parts of them
+    (40, 8, 8, 1, 128, 64, False, [128] * 40),               # more equal units than blocks
+    (37, 8, 4, 2, 64, 32, True, [96] * 37),
 ]
 
 
@@ -408,6 +414,40 @@ def test_evict_many_protected_rows():
     attn.kv_cache_evict(k, v, table, Pd, w, pos, torch.tensor([100], dtype=torch.int32, device="cuda"), keep, recent=5)
     torch.cuda.synchronize()
     assert Pd.item() == keep and torch.equal(w[0, 0, :keep], w0[0, 0, :keep])
+
+
+# ------------------------------------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("S,d", [(1, 128), (16, 128), (1, 64), (9, 32)])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_clean(S, d):
+    """The test hook shortens the waits to 1 ms and holds the loads back for 20 ms: the calls return, the error
+    says so, and with a zero-filled workspace the next call is right."""
+    lib = _lib.load()
+    cache = R.Cache(2, 2, d, 16, [700, 90], 700, 6950)
+    q = R.bf16((2, 8, S, d), 6951)
+    qd = q.cuda()
+    k, v, table, P = cache.cuda()
+    ws = attn.sample_paged_workspace(qd, k)
+    lse = torch.zeros(2, 8, S, device="cuda")
+    w = torch.zeros(2, 2, cache.capacity, device="cuda")
+    torch.cuda.synchronize()
+    assert attn.last_device_error() == 0
+    for call in (lambda: attn.decoder_sample_paged(qd, k, v, table, P, workspace=ws),
+                 lambda: attn.kv_cache_weigh(qd, k, table, P, lse, w)):
+        try:
+            assert lib.e2d2_debug_set_wait_test(1_000_000, 20_000_000) == 0
+            call()
+            torch.cuda.synchronize()
+            assert attn.last_device_error() == E2D2_ERR_TIMEOUT
+        finally:
+            assert lib.e2d2_debug_set_wait_test(0, 0) == 0
+    got = attn.decoder_sample_paged(qd, k, v, table, P, workspace=ws.zero_())
+    w.zero_()
+    attn.kv_cache_weigh(qd, k, table, P, got[1], w)
+    torch.cuda.synchronize()
+    assert attn.last_device_error() == 0
+    R.check_sample(got, R.sample(cache, q, None, None), "after a timed-out call")
+    ref, tol = R.weigh(cache, q, got[1].cpu(), torch.zeros(2, 2, cache.capacity))
+    assert (np.abs(w.cpu().numpy() - ref) <= tol).all()
 
 
 # ------------------------------------------------------------------------------------------------ together
