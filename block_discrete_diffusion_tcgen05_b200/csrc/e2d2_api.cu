@@ -1032,8 +1032,8 @@ template <int D, int N>
 e2d2_status launch_weigh(const WeighParams& a, const DeviceInfo* di, cudaStream_t stream) {
     using C = WeighCfg<D, N>;
     auto kern = kv_weigh_kernel<D, N>;
-    // at least ~116 KB, so that no two blocks share an SM: at N = 256 each takes all of its tensor memory
-    const int smem = C::ALLOC > 118784 ? C::ALLOC : 118784;
+    // one block per SM: at least ~116 KB, so that no two share it (at N = 256 each takes all of its tensor memory)
+    const int smem = C::CTAS == 2 || C::ALLOC > 118784 ? C::ALLOC : 118784;
     static thread_local int configured_dev = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1042,7 +1042,7 @@ e2d2_status launch_weigh(const WeighParams& a, const DeviceInfo* di, cudaStream_
             return E2D2_ERR_CUDA;
         configured_dev = dev;
     }
-    return launch_pdl(kern, dim3(di->sms), dim3(kWeighThreads), smem, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
+    return launch_pdl(kern, dim3(C::CTAS * di->sms), dim3(kWeighThreads), smem, stream, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
 }
 
 template <int D>

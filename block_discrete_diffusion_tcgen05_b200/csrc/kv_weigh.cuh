@@ -49,8 +49,9 @@ struct WeighCfg {
     static constexpr uint32_t SWZ = RB == 128 ? 2u : 4u;
     static constexpr int QCHUNK = N * RB, Q_BYTES = NCH * QCHUNK;
     static constexpr int KCHUNK = kWeighKeys * RB, K_BYTES = NCH * KCHUNK;
-    static constexpr int QB = N <= 64 ? 2 : 1;
-    static constexpr int FIT = (216 * 1024 - QB * Q_BYTES) / K_BYTES;
+    static constexpr int CTAS = N == 32 ? 2 : 1;  // blocks per SM
+    static constexpr int QB = N == 64 ? 2 : 1;
+    static constexpr int FIT = ((CTAS == 2 ? 109 : 216) * 1024 - QB * Q_BYTES) / K_BYTES;
     static constexpr int NST = FIT < 8 ? FIT : 8;
     static constexpr uint32_t TMEM_COLS = 2 * N < 32 ? 32u : 2u * N;
     static constexpr int OFF_Q = 0;
@@ -120,7 +121,7 @@ struct WeighWalk {
 };
 
 template <int D, int N>
-__global__ void __launch_bounds__(kWeighThreads, 1) kv_weigh_kernel(const __grid_constant__ WeighParams p) {
+__global__ void __launch_bounds__(kWeighThreads, WeighCfg<D, N>::CTAS) kv_weigh_kernel(const __grid_constant__ WeighParams p) {
     using C = WeighCfg<D, N>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
