@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
 // blockIdx.y: (entry, kv head).  A warp takes eight moves at a time: lane l looks up where row l comes from and goes
 // to.  VPR: 16-byte vectors per row.
 template <int VPR>
-__global__ void __launch_bounds__(256) kv_evict_move_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(256, 4) kv_evict_move_kernel(const __grid_constant__ EvictParams p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int unit = blockIdx.y, Hkv = p.pages.kv_heads, lane = threadIdx.x & 31;
@@ -280,10 +280,14 @@ __global__ void __launch_bounds__(256) kv_evict_move_kernel(const __grid_constan
     const int moves = __ldcg(ws);
     const uint4* const src[2] = {p.pool[0], p.pool[1]};
     for (int m0 = (blockIdx.x * 8 + threadIdx.x / 32) * 8; m0 < moves; m0 += gridDim.x * 64) {
-        long long from = -1, to = -1;
+        uint32_t from = kNoRow, to = kNoRow;
         if (lane < 8 && m0 + lane < moves) {
-            from = p.pages.pool_row(b, h, __ldcg(mover_list + m0 + lane));
-            to = p.pages.pool_row(b, h, __ldcg(hole_list + m0 + lane));
+            const int s = __ldcg(mover_list + m0 + lane), d = __ldcg(hole_list + m0 + lane);
+            int s_in, d_in;
+            const int s_e = p.pages.entry(b, s, s_in), d_e = p.pages.entry(b, d, d_in);  // both loads before a look at either
+            const int s_pg = p.pages.page(s_e), d_pg = p.pages.page(d_e);
+            if (s_pg >= 0) from = static_cast<uint32_t>((static_cast<long long>(s_pg) * Hkv + h) * p.pages.page_rows + s_in);
+            if (d_pg >= 0) to = static_cast<uint32_t>((static_cast<long long>(d_pg) * Hkv + h) * p.pages.page_rows + d_in);
         }
         copy_rows8<VPR>(src, p.pool, from, to);
     }

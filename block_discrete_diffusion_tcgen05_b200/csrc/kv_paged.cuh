@@ -136,26 +136,28 @@ __device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar, int lane) {
 }
 
 // Copies rows of K and V, eight at a time, by one warp: lane l < 8 gives the rows (of VPR 16-byte vectors) that move
-// l reads and writes, -1 for none.  K and V of one row (of two, four at smaller head dims) are the warp's 32 vectors;
-// all of the eight are loaded before the first is stored.
+// l reads and writes, kNoRow for none (a row number fits in 32 bits: 2^32 rows of d = 32 are more than the memory).  K
+// and V of one row (of two, four at smaller head dims) are the warp's 32 vectors; all of the eight are loaded before
+// the first is stored.
+constexpr uint32_t kNoRow = 0xffffffffu;
 template <int VPR>
-__device__ __forceinline__ void copy_rows8(const uint4* const (&src)[2], uint4* const (&dst)[2], long long from, long long to) {
+__device__ __forceinline__ void copy_rows8(const uint4* const (&src)[2], uint4* const (&dst)[2], uint32_t from, uint32_t to) {
     constexpr int RPS = 16 / VPR, STEPS = 8 / RPS;  // rows per step, steps
     const int lane = threadIdx.x & 31, which = (lane / VPR) & 1, vec = lane % VPR, sub = lane / (2 * VPR);
-    const uint4* s_base = which ? src[1] : src[0];
-    uint4* d_base = which ? dst[1] : dst[0];
-    if (from < 0) to = -1;
+    const uint4* s_base = (which ? src[1] : src[0]) + vec;
+    uint4* d_base = (which ? dst[1] : dst[0]) + vec;
+    if (from == kNoRow) to = kNoRow;
     uint4 x[STEPS];
-    uint4* d[STEPS];
+    uint32_t d[STEPS];
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
-        const long long s = __shfl_sync(0xffffffffu, from, k * RPS + sub), t = __shfl_sync(0xffffffffu, to, k * RPS + sub);
-        d[k] = t < 0 ? nullptr : d_base + t * VPR + vec;
-        if (t >= 0) x[k] = __ldcg(s_base + s * VPR + vec);
+        const uint32_t s = __shfl_sync(0xffffffffu, from, k * RPS + sub);
+        d[k] = __shfl_sync(0xffffffffu, to, k * RPS + sub);
+        if (d[k] != kNoRow) x[k] = __ldcg(s_base + static_cast<size_t>(s) * VPR);
     }
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
-        if (d[k] != nullptr) *d[k] = x[k];
+        if (d[k] != kNoRow) d_base[static_cast<size_t>(d[k]) * VPR] = x[k];
 }
 
 struct PagedAppendParams {
@@ -171,14 +173,14 @@ struct PagedAppendParams {
 
 // A pure copy, HBM-bound: a warp per eight new rows, grid-stride.
 template <int VPR>
-__global__ void __launch_bounds__(256) kv_append_paged_kernel(const __grid_constant__ PagedAppendParams a) {
+__global__ void __launch_bounds__(256, 4) kv_append_paged_kernel(const __grid_constant__ PagedAppendParams a) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();  // the previous kernel may still read the pool or write the new rows
     const int Hkv = a.pages.kv_heads, cap = a.pages.capacity(), lane = threadIdx.x & 31;
     const long long total = static_cast<long long>(a.batch) * Hkv * a.S_new;
     for (long long r0 = (blockIdx.x * 8ll + threadIdx.x / 32) * 8; r0 < total; r0 += gridDim.x * 64ll) {
         const long long from = r0 + lane;
-        long long to = -1;
+        uint32_t to = kNoRow;
         if (lane < 8 && from < total) {
             const int unit = static_cast<int>(from / a.S_new), s = static_cast<int>(from - static_cast<long long>(unit) * a.S_new);
             const int b = unit / Hkv, h = unit - b * Hkv;
@@ -189,10 +191,10 @@ __global__ void __launch_bounds__(256) kv_append_paged_kernel(const __grid_const
                     a.weight[w] = 0.f;
                     a.pos[w] = __ldcg(a.tokens + b) + s;
                 }
-                to = a.pages.pool_row(b, h, static_cast<int>(r));
+                to = static_cast<uint32_t>(a.pages.pool_row(b, h, static_cast<int>(r)));  // -1: kNoRow
             }
         }
-        copy_rows8<VPR>(a.src, a.pool, from, to);
+        copy_rows8<VPR>(a.src, a.pool, static_cast<uint32_t>(from), to);
     }
 }
 
