@@ -381,15 +381,15 @@ def kv_cache_append_ragged(k_cache, v_cache, P, k_new, v_new):
 def _pages(k_pages: torch.Tensor, page_table, batch: int):
     """The e2d2_pages of a pool [num_pages, Hkv, page_rows, d] and its table (CUDA int32
     [batch, max_pages]; None: contiguous caches, one page per entry), and the row capacity."""
-    num_pages, page_rows = k_pages.shape[0], k_pages.shape[2]
+    num_pages, _, page_rows, _ = k_pages.shape
     if page_table is None:
         if num_pages != batch:
             raise ValueError("without a page table the caches must be [B, Hkv, capacity, d]")
         return _lib.Pages(num_pages, page_rows, 1, None), page_rows
-    _need(page_table, "page_table", dtype=_I32, ndim=2)
-    if page_table.shape[0] != batch:
+    _need(page_table, "page_table", _I32, 2)
+    rows, max_pages = page_table.shape
+    if rows != batch:
         raise ValueError("page_table must be [B, max_pages]")
-    max_pages = page_table.shape[1]
     return _lib.Pages(num_pages, page_rows, max_pages, page_table.data_ptr()), max_pages * page_rows
 
 
@@ -444,11 +444,10 @@ def decoder_sample_paged(q_blk, k_pages, v_pages, page_table, P, k_blk=None, v_b
             raise ValueError("k_blk/v_blk must be [B, Hkv, S, d]")
     ws = sample_paged_workspace(q_blk, k_pages) if workspace is None else _need_workspace(workspace)
     out = _out_tensor(out, q_blk)
-    lse_t = _lse_tensor(lse, (B, Hq, S), q_blk.device)
+    lse_t = q_blk.new_empty((B, Hq, S), dtype=_F32) if lse is True else _lse_tensor(lse, (B, Hq, S), q_blk.device)
     st = lib.e2d2_attn_decoder_sample_paged(q_blk.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages,
                                             P.data_ptr(), _ptr(k_blk), _ptr(v_blk), out.data_ptr(), _ptr(lse_t),
-                                            _dims(B, Hq, Hkv, d, scale), S, ws.data_ptr(),
-                                            ws.numel() * ws.element_size(), _stream(q_blk))
+                                            _dims(B, Hq, Hkv, d, scale), S, ws.data_ptr(), ws.nbytes, _stream(q_blk))
     _lib.check(st, "e2d2_attn_decoder_sample_paged")
     return out, lse_t
 
@@ -461,12 +460,13 @@ def kv_cache_append_paged(k_pages, v_pages, page_table, P, k_new, v_new, weight=
     lib = _lib.load()
     for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_new, "k_new"), (v_new, "v_new")):
         _need(t, n)
-    B, Hkv, S_new, d = k_new.shape
-    if k_pages.shape[1] != Hkv or k_pages.shape[3] != d or v_pages.shape != k_pages.shape or v_new.shape != k_new.shape:
+    shape, new = k_pages.shape, k_new.shape
+    B, Hkv, S_new, d = new
+    if shape[1] != Hkv or shape[3] != d or v_pages.shape != shape or v_new.shape != new:
         raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_rows, d], k_new/v_new [B, Hkv, S_new, d]")
     pages, cap = _pages(k_pages, page_table, B)
     _need_ints(P, "P", B)
-    if len({weight is None, pos is None, tokens is None}) != 1:
+    if (weight is None) != (pos is None) or (weight is None) != (tokens is None):
         raise ValueError("weight, pos and tokens must be given together")
     if weight is not None:
         _need_rows(weight, "weight", (B, Hkv, cap), torch.float32)
@@ -495,11 +495,11 @@ def kv_cache_weigh(q, k_pages, page_table, P, lse, weight, out=None, scale=None)
     _need(lse, "lse", dtype=torch.float32, ndim=3)
     if lse.shape != (B, Hq, S):
         raise ValueError("lse must be [B, Hq, S]")
-    _need_rows(weight, "weight", (B, Hkv, cap), torch.float32)
+    _need_rows(weight, "weight", (B, Hkv, cap), _F32)
     if out is None:
         out = weight
     else:
-        _need_rows(out, "out", (B, Hkv, cap), torch.float32)
+        _need_rows(out, "out", (B, Hkv, cap), _F32)
     st = lib.e2d2_kv_cache_weigh(q.data_ptr(), k_pages.data_ptr(), pages, P.data_ptr(), lse.data_ptr(),
                                  weight.data_ptr(), out.data_ptr(), _dims(B, Hq, Hkv, d, scale), S, _stream(q))
     _lib.check(st, "e2d2_kv_cache_weigh")
@@ -540,10 +540,15 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
     weight_out = weight if weight_out is None else weight_out
     pos_out = pos if pos_out is None else pos_out
     P_out = P if P_out is None else P_out
-    for t, n, dt in ((weight, "weight", torch.float32), (weight_out, "weight_out", torch.float32),
-                     (pos, "pos", torch.int32), (pos_out, "pos_out", torch.int32)):
-        _need_rows(t, n, (B, Hkv, cap), dt)
-    _need_ints(P_out, "P_out", B)
+    rows = (B, Hkv, cap)
+    _need_rows(weight, "weight", rows, _F32)
+    _need_rows(pos, "pos", rows, _I32)
+    if weight_out is not weight:
+        _need_rows(weight_out, "weight_out", rows, _F32)
+    if pos_out is not pos:
+        _need_rows(pos_out, "pos_out", rows, _I32)
+    if P_out is not P:
+        _need_ints(P_out, "P_out", B)
     ws = evict_workspace(weight) if workspace is None else _need_workspace(workspace)
     st = lib.e2d2_kv_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), pages, P.data_ptr(), weight.data_ptr(),
                                  pos.data_ptr(), tokens.data_ptr(), int(keep), int(recent), weight_out.data_ptr(),
