@@ -39,16 +39,16 @@ struct TcCfg {
     static constexpr int Q_BYTES = N * D * 2;
     static constexpr int P_CHUNKS = (2 * N + 63) / 64;  // 64-column chunks of [P^T | R^T]
     static constexpr int P_BYTES = P_CHUNKS * HALF;
-    static constexpr int NK = N == 64 ? 2 : 3, NV = 3;  // ring stages
+    static constexpr int NK = N == 64 ? 2 : 3, NV = 2;  // ring stages; [P^T | R^T] is double-buffered
     static constexpr uint32_t TMEM_COLS = 4 * N;      // S^T at 0 and N, O^T at 2 N
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
-    static constexpr int OFF_K = OFF_P + P_BYTES;
+    static constexpr int OFF_K = OFF_P + 2 * P_BYTES;
     static constexpr int OFF_V = OFF_K + NK * KV;
     static constexpr int OFF_BAR = OFF_V + NV * KV;
-    // q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[2], s_free[2], p_full, pv_done, o_free,
-    // s_drain, pv_drain, done
-    static constexpr int NBAR = 2 + 2 * NK + 2 * NV + 4 + 6;
+    // q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[2], s_free[2], p_full[2], pv_done[2],
+    // o_free, s_drain, pv_drain, done
+    static constexpr int NBAR = 2 + 2 * NK + 2 * NV + 8 + 4;
     static constexpr int OFF_CMAX = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // float [WGS][2 parity][4 warps][NH]
     static constexpr int OFF_LRED = OFF_CMAX + WGS * 2 * 4 * NH * 4;      // float [WGS][4 warps][NH]
     static constexpr int OFF_MISC = OFF_LRED + WGS * 4 * NH * 4;          // holder, abort, broadcast
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
     uint64_t* s_full = v_empty + C::NV;
     uint64_t* s_free = s_full + 2;
     uint64_t* p_full = s_free + 2;
-    uint64_t* pv_done = p_full + 1;
-    uint64_t* o_free = pv_done + 1;
+    uint64_t* pv_done = p_full + 2;
+    uint64_t* o_free = pv_done + 2;
     uint64_t* s_drain = o_free + 1;
     uint64_t* pv_drain = s_drain + 1;
     uint64_t* done = pv_drain + 1;
@@ -104,8 +104,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
         for (int i = 0; i < C::NK; ++i) ptx::mbar_init(&k_full[i], 1), ptx::mbar_init(&k_empty[i], 1);
         for (int i = 0; i < C::NV; ++i) ptx::mbar_init(&v_full[i], 1), ptx::mbar_init(&v_empty[i], 1);
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&s_full[i], 1), ptx::mbar_init(&s_free[i], 4 * C::WGS);
-        ptx::mbar_init(p_full, 4 * C::WGS);
-        ptx::mbar_init(pv_done, 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&p_full[i], 4 * C::WGS), ptx::mbar_init(&pv_done[i], 1);
         ptx::mbar_init(o_free, 4 * C::WGS);
         ptx::mbar_init(s_drain, 1);
         ptx::mbar_init(pv_drain, 1);
@@ -261,7 +260,8 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
             if (walk.n == 0) continue;
             for (int i = 0; i < walk.n && ok; ++i) {
                 const uint32_t st = it % C::NV;
-                ok = wait_stage_warp(p_full, it & 1, abort_flag, p.err) &&
+                const uint32_t sb = it & 1;
+                ok = wait_stage_warp(&p_full[sb], (it >> 1) & 1, abort_flag, p.err) &&
                      (i > 0 || wait_stage_warp(o_free, (units & 1) ^ 1, abort_flag, p.err)) &&
                      wait_stage_warp(&v_full[st], (it / C::NV) & 1, abort_flag, p.err);
                 if (!ok) break;
@@ -269,12 +269,12 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 bool is_own;
                 const int steps = (min(kTcKeys, tile_rows(walk.c0 + i, is_own)) + 15) / 16;
                 if (leader) {
-                    const uint32_t v = sV + st * C::KV;
+                    const uint32_t v = sV + st * C::KV, pr = sP + sb * C::P_BYTES;
                     for (int ks = 0; ks < steps; ++ks)
-                        ptx::mma_ss(tmem + 2 * N, desc | ((v + ks * 16 * 128) >> 4), desc | ((sP + ks * 16 * 128) >> 4), idesc,
+                        ptx::mma_ss(tmem + 2 * N, desc | ((v + ks * 16 * 128) >> 4), desc | ((pr + ks * 16 * 128) >> 4), idesc,
                                     i > 0 || ks > 0 ? 1u : 0u);
                     ptx::mma_commit(&v_empty[st]);
-                    ptx::mma_commit(pv_done);
+                    ptx::mma_commit(&pv_done[sb]);
                 }
                 __syncwarp();
                 ++it;
@@ -332,7 +332,6 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < NH; ++j) top = fmaxf(top, fmaf(x[j], p.scale_log2, neg_m[j]));
-                bool waited = tc == 0;  // the last tile's product has read P^T and landed in O^T
                 if (barrier_any(1 + g, 128, top > kRescaleThreshold)) {
                     // new maxima, of every column whose keys reach past the old one
                     float tmp[NH];
@@ -342,10 +341,9 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                     float* cm = cmax + sb * 4 * NH;
                     if ((lane % (32 / NH)) == 0) cm[w * NH + lane / (32 / NH)] = mine;
                     ptx::named_barrier_sync(1 + g, 128);
-                    if (!waited) {
-                        wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
+                    if (i > 0) {  // O^T holds every product up to the last tile's once that one has landed
+                        wait_stage_warp(&pv_done[sb ^ 1], ((tc - 1) >> 1) & 1, abort_flag, p.err);
                         ptx::tc_fence_after();
-                        waited = true;
                     }
 #pragma unroll
                     for (int c8 = 0; c8 < NH; c8 += 8) {
@@ -386,13 +384,15 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                     hi[j / 2] = h2;
                     lo[j / 2] = ptx::pack_bf16x2(e0 - __uint_as_float(h2 << 16), e1 - __uint_as_float(h2 & 0xffff0000u));
                 }
-                if (!waited) wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
+                // the buffer was read by the product of the tile before last
+                wait_stage_warp(&pv_done[sb], ((tc >> 1) & 1) ^ 1, abort_flag, p.err);
+                uint8_t* pr = sP + sb * C::P_BYTES;
 #pragma unroll
                 for (int u = 0; u < NH / 8; ++u) {
                     const int uh = g * (NH / 8) + u, ul = N / 8 + uh;  // 16-byte units of the row
-                    *reinterpret_cast<uint4*>(sP + uh / 8 * C::HALF + swz_rows<128>(key, uh % 8)) =
+                    *reinterpret_cast<uint4*>(pr + uh / 8 * C::HALF + swz_rows<128>(key, uh % 8)) =
                         make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-                    *reinterpret_cast<uint4*>(sP + ul / 8 * C::HALF + swz_rows<128>(key, ul % 8)) =
+                    *reinterpret_cast<uint4*>(pr + ul / 8 * C::HALF + swz_rows<128>(key, ul % 8)) =
                         make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
                 }
                 if (g == 0 && !is_own && valid < kTcKeys && (valid & 15) != 0) {
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
-                mbar_arrive_warp(p_full, lane);
+                mbar_arrive_warp(&p_full[sb], lane);
             }
             // ---- the unit's end: column sums over the keys, O^T out of tensor memory
             const bool whole = walk.whole;
@@ -442,14 +442,14 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 }
             }
             if (walk.n > 0) {
-                wait_stage_warp(pv_done, (tc - 1) & 1, abort_flag, p.err);
+                wait_stage_warp(&pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, abort_flag, p.err);
                 ptx::tc_fence_after();
             }
             if (whole) ptx::named_barrier_sync(1 + g, 128);  // inv_l is written
             const int cols = min(NH, rows_here - g * NH);    // rows of this warpgroup's columns
             __nv_bfloat16* out = p.out + (walk.row0 + g * NH) * D + key;
             float* part = whole ? nullptr : slot + g * NH * D + key;
-#pragma unroll
+#pragma unroll 1
             for (int c8 = 0; c8 < NH; c8 += 8) {
                 uint32_t oh[8], ol[8];
                 if (walk.n > 0) {
