@@ -492,7 +492,9 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 ptx::named_barrier_sync(1 + C::WGS, C::SOFT);  // read before the next unit's is written
                 if (join) {
                     __threadfence();
-                    join_parts<D, 4 * C::WGS, 2, 4>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
+                    // few rows: many parts in flight (token, 18 parts: 14.8 against 17.8 us for the call); many rows: many rows
+                    // (64 rows, 5 parts: 105 against 108 us)
+                    join_parts<D, 4 * C::WGS, N == 16 ? 1 : 4, N == 16 ? 8 : 2>(p, walk.slot(c_first, c_first), walk.slot(c_first + 1, c_first), c_last - c_first + 1,
                                            walk.row0, rows_here, warp - 4, lane);
                 }
             }
