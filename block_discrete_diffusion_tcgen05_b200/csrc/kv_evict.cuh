@@ -14,6 +14,10 @@
 // memory); eleven bits tell weights apart that share an exponent, so few lanes meet in a bin, and a pass whose bin
 // stays whole is the last.  Then every warp counts the holes and movers of its rows, and their places in the lists
 // follow from the counts ahead of it: no sort, and no order that depends on timing.
+//
+// Select is bound by its own steps, a dozen block-wide ones of about a microsecond: 32 heads of 32768 rows take 22 us
+// on clusters of four (54 us on one block each), 256 heads of 2064 rows 11 us.  Move is bound by HBM in rows of 256
+// bytes: 198 MB read and written take 38 us, 5.2 TB/s.
 #pragma once
 
 #include <cstdint>

@@ -11,7 +11,9 @@
 // Warp 0 loads (a ring of key tiles of 128 rows, in boxes that end where pages do; Q once per unit), warp 1
 // issues the products into two buffers of tensor memory, and two warpgroups take the tiles in turn: one reads
 // its scores while the other's are computed.  The tiles of all (entry, kv head) units form one stream cut
-// evenly over a persistent grid.
+// evenly over a persistent grid.  Up to 32 query rows two blocks share an SM, so one starts or changes units while the
+// other streams: 32 blocks of 16 tokens over 2064 rows (32 query rows per head) take 28 us, 5.0 TB/s, against 32 us
+// with one block per SM.
 #pragma once
 
 #include <cstdint>

@@ -175,7 +175,7 @@ __device__ __forceinline__ int paged_parts(unsigned total, unsigned units, bool 
 
 // Four columns of an output row from their weighted sum and the sum of the weights.
 __device__ __forceinline__ void write_row4(const PagedAttnParams& p, long long at, int D, int q4, float l, const float4& acc) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing: zeros
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros (NaN stays NaN)
     uint2 w;
     w.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
     w.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
@@ -259,7 +259,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnParams& p, const float
             if (base + WARPS * RPW * y + lane / LPR < rows) {
                 write_row4(p, row0 + row[y], D, li, lt[y], acc[y]);
                 if (li == 0 && p.lse != nullptr)
-                    p.lse[row0 + row[y]] = lt[y] > 0.f ? (mt[y] + log2f(lt[y])) * 0.69314718055994531f : -INFINITY;
+                    p.lse[row0 + row[y]] = lt[y] == 0.f ? -INFINITY : (mt[y] + log2f(lt[y])) * 0.69314718055994531f;
             }
     }
 }
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                 if (whole) {
                     write_row4(p, row0 + row, D, q4, lt, acc);
                     if (q4 == 0 && p.lse != nullptr)
-                        p.lse[row0 + row] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                        p.lse[row0 + row] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
                 } else {
                     __stcg(reinterpret_cast<float4*>(slot + row * D) + q4, acc);
                     if (q4 == 0) {

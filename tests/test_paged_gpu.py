@@ -175,6 +175,24 @@ def test_bad_pages_are_left_out_and_reported():
         assert attn.last_device_error() == 0
 
 
+@pytest.mark.parametrize("d,S,P", [(128, 1, 100), (128, 16, 900), (64, 1, 100), (64, 9, 900), (32, 3, 900)])
+def test_nan_in_a_row_in_use_reaches_what_uses_it_and_nothing_else(d, S, P):
+    cache = R.Cache(2, 2, d, 16, [P, 50], P, 5850)
+    pg, i = cache.where(0, 37)
+    cache.k[pg, 0, i, 3] = float("nan")     # entry 0, kv head 0: every score against row 37
+    cache.v[pg, 1, i, 5] = float("nan")     # entry 0, kv head 1: one column of the values
+    q = R.bf16((2, 8, S, d), 5851)
+    k, v, table, Pd = cache.cuda()
+    out, lse = attn.decoder_sample_paged(q.cuda(), k, v, table, Pd)
+    w = attn.kv_cache_weigh(q.cuda(), k, table, Pd, torch.zeros_like(lse), torch.zeros(2, 2, cache.capacity, device="cuda"))
+    torch.cuda.synchronize()
+    assert out[0, :4].isnan().all() and lse[0, :4].isnan().all()
+    assert out[0, 4:, :, 5].isnan().all() and not out[0, 4:, :, :5].isnan().any() and not out[0, 4:, :, 6:].isnan().any()
+    assert torch.isfinite(lse[0, 4:]).all() and torch.isfinite(out[1].float()).all() and torch.isfinite(lse[1]).all()
+    assert w[0, 0, 37].isnan() and torch.isfinite(w[0, 0, :37]).all() and torch.isfinite(w[0, 0, 38:]).all()
+    assert torch.isfinite(w[0, 1]).all() and torch.isfinite(w[1]).all()
+
+
 def test_shared_pages_are_read_by_both_entries():
     cache = R.Cache(2, 2, 128, 16, [90, 70], 96, 5800)
     cache.table[1, :4] = cache.table[0, :4]   # a common prefix of 64 tokens
