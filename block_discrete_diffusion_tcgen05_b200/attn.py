@@ -515,9 +515,9 @@ def evict_workspace_bytes(batch, kv_heads, row_capacity) -> int:
 
 @_device_guard
 def evict_workspace(weight: torch.Tensor) -> torch.Tensor:
-    """A workspace for kv_cache_evict with weight [B,Hkv,row capacity]."""
+    """A zero-filled workspace for kv_cache_evict with weight [B,Hkv,row capacity]."""
     B, Hkv, cap = weight.shape
-    return torch.empty(max(evict_workspace_bytes(B, Hkv, cap), 16), dtype=torch.uint8, device=weight.device)
+    return torch.zeros(max(evict_workspace_bytes(B, Hkv, cap), 16), dtype=torch.uint8, device=weight.device)
 
 
 @_device_guard

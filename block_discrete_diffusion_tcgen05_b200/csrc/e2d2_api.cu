@@ -1068,9 +1068,9 @@ PagedLayout paged_layout(const e2d2_dims& dims, int S) {
 }
 static_assert(kPagedMaxCtas * sizeof(int) <= 2048, "tickets");
 
-template <int THREADS>
-e2d2_status launch_evict_select(const EvictParams& a, unsigned units, unsigned cluster, cudaStream_t stream) {
-    auto kern = kv_evict_select_kernel<THREADS>;
+template <int THREADS, int VPR>
+e2d2_status launch_evict(const EvictParams& a, unsigned units, unsigned cluster, cudaStream_t stream) {
+    auto kern = kv_evict_kernel<THREADS, VPR>;
     static thread_local int configured_dev = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1095,11 +1095,22 @@ e2d2_status launch_evict_select(const EvictParams& a, unsigned units, unsigned c
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
 }
 
+template <int THREADS>
+e2d2_status launch_evict_rows(int head_dim, const EvictParams& a, unsigned units, unsigned cluster, cudaStream_t stream) {
+    switch (head_dim) {
+        case 32: return launch_evict<THREADS, 4>(a, units, cluster, stream);
+        case 64: return launch_evict<THREADS, 8>(a, units, cluster, stream);
+        default: return launch_evict<THREADS, 16>(a, units, cluster, stream);
+    }
+}
+
 // Rows that one list of an eviction can hold, rounded to whole 16 bytes.
 long long evict_list_rows(const e2d2_pages& pg) { return (row_capacity(pg) / 2 + 4) / 4 * 4; }
 
+constexpr size_t kEvictHeader = 4;  // ints ahead of the lists: the count of heads done, for any dims
+
 size_t evict_workspace_bytes(const e2d2_dims& dims, const e2d2_pages& pg) {
-    return static_cast<size_t>(dims.batch) * dims.kv_heads * (4 + 2 * evict_list_rows(pg)) * sizeof(int);
+    return (kEvictHeader + static_cast<size_t>(dims.batch) * dims.kv_heads * 2 * evict_list_rows(pg)) * sizeof(int);
 }
 
 }  // namespace
@@ -1307,12 +1318,13 @@ e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, 
     a.weight_out = weight_out;
     a.pos_out = pos_out;
     a.P_out = P_out;
-    a.ws = static_cast<int*>(workspace);
+    a.heads_done = static_cast<int*>(workspace);
+    a.ws = a.heads_done + kEvictHeader;
     a.batch = dims.batch;
     a.keep = keep;
     a.recent = recent;
     a.list_rows = static_cast<int>(evict_list_rows(pages));
-    a.ws_stride = 4 + 2ll * a.list_rows;
+    a.ws_stride = 2ll * a.list_rows;
     const unsigned units = static_cast<unsigned>(dims.batch) * dims.kv_heads;
     const long long cap = row_capacity(pages);
     // blocks per (entry, kv head): as many as leave each 2048 rows and all of them a place on the GPU at once
@@ -1320,20 +1332,8 @@ e2d2_status e2d2_kv_cache_evict(void* k_pages, void* v_pages, e2d2_pages pages, 
     while (cluster < 8 && units * cluster * 2 <= static_cast<unsigned>(di->sms) && cap / (cluster * 2) >= 2048) cluster *= 2;
     const long long slice = ((cap + cluster - 1) / cluster + 31) / 32 * 32;
     a.rank_rows = static_cast<int>(slice < kEvictRows ? slice : kEvictRows);
-    s = slice <= 4096 ? launch_evict_select<512>(a, units, cluster, stream) : launch_evict_select<1024>(a, units, cluster, stream);
-    if (s != E2D2_OK) return s;
-    // eight moves per warp and round, at most eight blocks per SM
-    const long long most = (a.list_rows + 63) / 64;
-    long long x = (di->sms * 8 + units - 1) / units;
-    if (x > most) x = most;
-    const dim3 grid(static_cast<unsigned>(x), units);
-    cudaError_t e;
-    switch (dims.head_dim) {
-        case 32: e = launch_pdl(kv_evict_move_kernel<4>, grid, dim3(256), 0, stream, a); break;
-        case 64: e = launch_pdl(kv_evict_move_kernel<8>, grid, dim3(256), 0, stream, a); break;
-        default: e = launch_pdl(kv_evict_move_kernel<16>, grid, dim3(256), 0, stream, a); break;
-    }
-    return e == cudaSuccess ? E2D2_OK : E2D2_ERR_CUDA;
+    return slice <= 4096 ? launch_evict_rows<512>(dims.head_dim, a, units, cluster, stream)
+                         : launch_evict_rows<1024>(dims.head_dim, a, units, cluster, stream);
 }
 
 }  // extern "C"

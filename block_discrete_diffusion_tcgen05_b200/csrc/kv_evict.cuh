@@ -7,17 +7,19 @@
 // overlap.  Attention over the prefix does not depend on the order of its rows; pos says which token each
 // one is.
 //
-// Two launches: select finds the kept rows and writes the lists of movers and holes, move copies the K and V rows
-// over the whole GPU.  Select takes a cluster of 1 to 8 blocks per (entry, kv head), each with a slice of the rows.
-// It reads 8 bytes a row once, keeps the slice's ranks in shared memory (up to 32768 rows), and finds the keep-th
-// largest by 11, 11 and 10 bits in turn, from histograms that the blocks read from each other (distributed shared
-// memory); eleven bits tell weights apart that share an exponent, so few lanes meet in a bin, and a pass whose bin
-// stays whole is the last.  Then every warp counts the holes and movers of its rows, and their places in the lists
-// follow from the counts ahead of it: no sort, and no order that depends on timing.
+// One launch: a cluster of 1 to 8 blocks per (entry, kv head), each with a slice of the rows.  It reads 8 bytes a row
+// once, keeps the slice's ranks in shared memory (up to 32768 rows), and finds the keep-th largest by 11, 11 and 10
+// bits in turn, from histograms that the blocks read from each other (distributed shared memory); eleven bits tell
+// weights apart that share an exponent, so few lanes meet in a bin, and a pass whose bin stays whole is the last.  Then
+// every warp counts the holes and movers of its rows, and their places in the lists follow from the counts ahead of
+// it: no sort, and no order that depends on timing.  The cluster's warps then move the rows, K and V, eight at a time.
+// The new lengths may lie where the old ones do: the last cluster to have read its own writes them all.
 //
-// Select is bound by its own steps, a dozen block-wide ones of about a microsecond: 32 heads of 32768 rows take 22 us
-// on clusters of four (54 us on one block each), 256 heads of 2064 rows 11 us.  Move is bound by HBM in rows of 256
-// bytes: 198 MB read and written take 38 us, 5.2 TB/s.
+// 256 heads of 2064 rows, 16 moves each: 12.9 us, bound by a dozen block-wide steps of about a microsecond.  32 heads of
+// 32768 rows to 8192 on clusters of four: 58 us, of which about 20 find the rows and 38 move 198 MB in rows of 256 bytes
+// (5.2 TB/s).  Two launches, the second moving the rows from the whole GPU, took 14.8 and 62 us, 2 to 3 us more outside a
+// graph, and were faster only where few heads leave SMs idle (8 heads of 32768 rows: 40.6 against 43.5).  64 registers,
+// so that 512-thread blocks share an SM in pairs: 22 us for the 256 heads without.
 #pragma once
 
 #include <cstdint>
@@ -40,7 +42,8 @@ struct EvictParams {
     float* weight_out;    // the same arrays, or others
     int* pos_out;
     int* P_out;
-    int* ws;              // per unit: count, kept length, 2 unused, then list_rows holes, list_rows movers
+    int* heads_done;      // zero between calls
+    int* ws;              // per unit: list_rows holes, list_rows movers
     int batch, keep, recent;
     int list_rows;
     int rank_rows;        // rows that the launch's shared memory has ranks for
@@ -68,8 +71,9 @@ __device__ __forceinline__ int warps_exclusive(int x, int* wsum, int* total) {
     return __reduce_add_sync(0xffffffffu, lane < wid ? mine : 0);
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_constant__ EvictParams p) {
+// VPR: 16-byte vectors per row of K or V.
+template <int THREADS, int VPR>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const __grid_constant__ EvictParams p) {
     namespace cg = cooperative_groups;
     constexpr int WARPS = THREADS / 32, BINS = 2048 / THREADS, BATCH = 8;
     __shared__ __align__(16) unsigned int hist[2][2048];
@@ -84,7 +88,7 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
     for (int i = tid; i < 2 * 2048; i += THREADS) (&hist[0][0])[i] = 0;
     ptx::griddep_wait();
     const int unit = blockIdx.x / blocks, Hkv = p.pages.kv_heads, cap = p.pages.capacity();
-    const int b = unit / Hkv;
+    const int b = unit / Hkv, h = unit - b * Hkv;
     const int P = ragged_clamp(__ldcg(p.P_dev + b), cap);
     // the first protected position, without overflow for any recent >= 0
     const long long pf = static_cast<long long>(__ldcg(p.tokens + b)) - p.recent;
@@ -98,17 +102,25 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
     const bool copy = w_out != w || pos_out != pos;
     const int per = ((P + blocks - 1) / blocks + 31) / 32 * 32;  // rows of a block
     const int beg = min(me * per, P), rows = min(beg + per, P) - beg;
-    const int kept = min(P, p.keep);
+    // By the cluster's last warp, which has the fewest rows to move, when all of the cluster has read the length.
+    auto head_done = [&]() {
+        int before = 0;
+        if (lane == 0) {
+            __threadfence();
+            before = atomicAdd(p.heads_done, 1);
+        }
+        if (__shfl_sync(0xffffffffu, before, 0) != p.batch * Hkv - 1) return;
+        __threadfence();
+        for (int e = lane; e < p.batch; e += 32) p.P_out[e] = min(ragged_clamp(__ldcg(p.P_dev + e), cap), p.keep);
+        if (lane == 0) *p.heads_done = 0;
+    };
     if (P <= p.keep) {  // the same for every block of the cluster
         if (copy)
             for (int j = beg + tid; j < beg + rows; j += THREADS) {
                 w_out[j] = __ldcg(w + j);
                 pos_out[j] = __ldcg(pos + j);
             }
-        if (me == 0 && tid == 0) {
-            ws[0] = 0;
-            ws[1] = kept;
-        }
+        if (me == blocks - 1 && wid == WARPS - 1) head_done();  // the length stays, so who reads it later reads the same
         return;
     }
     const bool held = rows <= p.rank_rows;
@@ -199,7 +211,7 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
     }
     // Rows above the threshold stay, and the first `need` of the `equal` rows at it.  A warp takes a run of the
     // block's rows, 32 at a time, in their order.
-    int* hole_list = ws + 4;
+    int* hole_list = ws;
     int* mover_list = hole_list + p.list_rows;
     const int run = ((rows + WARPS - 1) / WARPS + 31) / 32 * 32;
     const int i_beg = min(wid * run, rows), i_end = min(i_beg + run, rows);
@@ -264,26 +276,11 @@ __global__ void __launch_bounds__(THREADS) kv_evict_select_kernel(const __grid_c
         w_out[d] = __ldcg(w + s);
         pos_out[d] = __ldcg(pos + s);
     }
-    if (me == 0 && tid == 0) {
-        ws[0] = moves;
-        ws[1] = kept;
-    }
-}
-
-// blockIdx.y: (entry, kv head).  A warp takes eight moves at a time: lane l looks up where row l comes from and goes
-// to.  VPR: 16-byte vectors per row.
-template <int VPR>
-__global__ void __launch_bounds__(256, 4) kv_evict_move_kernel(const __grid_constant__ EvictParams p) {
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int unit = blockIdx.y, Hkv = p.pages.kv_heads, lane = threadIdx.x & 31;
-    const int b = unit / Hkv, h = unit % Hkv;
-    const int* ws = p.ws + unit * p.ws_stride;
-    const int* hole_list = ws + 4;
-    const int* mover_list = hole_list + p.list_rows;
-    const int moves = __ldcg(ws);
+    if (me == blocks - 1 && wid == WARPS - 1) head_done();
     const uint4* const src[2] = {p.pool[0], p.pool[1]};
-    for (int m0 = (blockIdx.x * 8 + threadIdx.x / 32) * 8; m0 < moves; m0 += gridDim.x * 64) {
+#pragma unroll 1
+    for (int m0 = (me * WARPS + wid) * 8; m0 < moves; m0 += blocks * WARPS * 8) {
+        // lane l < 8: where row l comes from and goes to
         uint32_t from = kNoRow, to = kNoRow;
         if (lane < 8 && m0 + lane < moves) {
             const int s = __ldcg(mover_list + m0 + lane), d = __ldcg(hole_list + m0 + lane);
@@ -295,8 +292,6 @@ __global__ void __launch_bounds__(256, 4) kv_evict_move_kernel(const __grid_cons
         }
         copy_rows8<VPR>(src, p.pool, from, to);
     }
-    // the lengths come last: P_out may be P_dev, which the first launch read
-    if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0) p.P_out[b] = __ldcg(ws + 1);
 }
 
 }  // namespace e2d2

@@ -420,6 +420,29 @@ def test_evict_long_cache():
     run_evict([40000], 39000, 500, Hkv=1, page=128, seed=6801)
 
 
+def test_evict_workspace_serves_other_batches():
+    """One workspace, zero-filled once, for calls of different batches and heads: the lengths, in place, come out
+    right in each (they are written when every head of the call has read them)."""
+    ws = None
+    for B, Hkv, P in ((5, 3, 300), (1, 1, 90), (40, 8, 300), (1, 1, 90), (5, 3, 300)):
+        cache = R.Cache(B, Hkv, 32, 16, [P - 3 * b for b in range(B)], 300, 6950 + B)
+        k, v, table, Pd = cache.cuda()
+        w = torch.rand(B, Hkv, cache.capacity, device="cuda")
+        pos = torch.arange(cache.capacity, dtype=torch.int32, device="cuda").expand(B, Hkv, -1).contiguous()
+        if ws is None:
+            big = torch.zeros(40, 8, cache.capacity, device="cuda")
+            ws = attn.evict_workspace(big)
+        tokens = Pd.clone()
+        want = torch.minimum(Pd, torch.tensor(200, device="cuda", dtype=torch.int32))
+        kept = [torch.topk(w[b, h, : P - 3 * b], min(200, P - 3 * b)).values.sort().values
+                for b in range(B) for h in range(Hkv)]
+        attn.kv_cache_evict(k, v, table, Pd, w, pos, tokens, 200, recent=0, workspace=ws)
+        assert torch.equal(Pd, want)
+        got = [w[b, h, : int(want[b])].sort().values for b in range(B) for h in range(Hkv)]
+        assert all(torch.equal(x, y) for x, y in zip(got, kept))
+    assert attn.last_device_error() == 0
+
+
 def test_evict_many_protected_rows():
     """More rows at or past the protected position than fit (a caller's positions need not be distinct): the
     lowest of them stay."""
