@@ -43,7 +43,7 @@ def _device_guard(fn):
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
-        first = args[0] if args else None
+        first = args[0] if args else next((a for a in kwargs.values() if isinstance(a, Tensor)), None)
         if isinstance(first, Tensor) and first.is_cuda:
             idx = first.get_device()
             for a in args:

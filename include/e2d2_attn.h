@@ -398,7 +398,7 @@ E2D2_API e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d
  *   past P_out[b] keep their bits and need not be kept.
  *   Every page of rows below P must be the entry's own (not shared).
  *   workspace: at least e2d2_kv_cache_evict_workspace(dims, pages) bytes, 16-byte aligned, zero-filled
- *   once; completed calls leave it reusable on the same stream.
+ *   once; completed calls leave it reusable by later evictions of any dims on the same stream.
  *   Calls that may run at the same time need different workspaces.
  */
 E2D2_API size_t e2d2_kv_cache_evict_workspace(e2d2_dims dims, e2d2_pages pages);

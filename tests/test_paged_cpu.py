@@ -1,6 +1,7 @@
 """The paged-cache calls without a GPU: what the C ABI refuses, with the status it documents and before
 anything touches a device; what the Python front-end refuses; and that the front-end hands every argument to
 the parameter of its name."""
+import contextlib
 import ctypes
 
 import pytest
@@ -289,3 +290,33 @@ def test_reference_eviction_on_a_case_by_hand():
     # recent = 1 protects row 5 (position 5 of 6 tokens); then rows 0 (5) and 2 (3, before row 4's 3)
     moves, w2, p2 = R.evict(6, w, pos, 6, 3, 1)
     assert moves == [(5, 1)] and w2.tolist() == [5, 9, 3] and p2.tolist() == [4, 5, 2]
+
+
+def test_a_call_by_keywords_has_its_tensors_device_checked_and_current(monkeypatch):
+    class OnDevice(torch.Tensor):
+        index = 1
+        is_cuda = True
+
+        def get_device(self):
+            return self.index
+
+    def tensor(index):
+        t = torch.zeros(1).as_subclass(OnDevice)
+        t.index = index
+        return t
+
+    entered = []
+
+    @contextlib.contextmanager
+    def device(idx):
+        entered.append(idx)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    call = attn._device_guard(lambda q, k: "ran")
+    assert call(tensor(1), tensor(1)) == "ran" and entered == [1]
+    assert call(q=None, k=tensor(1)) == "ran" and entered == [1, 1]
+    for kw in ({"q": tensor(1), "k": tensor(0)}, {"q": tensor(0), "k": torch.zeros(1)}):
+        with pytest.raises(ValueError, match="every tensor must be on"):
+            call(**kw)
