@@ -15,11 +15,11 @@
 // it: no sort, and no order that depends on timing.  The cluster's warps then move the rows, K and V, eight at a time.
 // The new lengths may lie where the old ones do: the last cluster to have read its own writes them all.
 //
-// 256 heads of 2064 rows, 16 moves each: 12.9 us, bound by a dozen block-wide steps of about a microsecond.  32 heads of
-// 32768 rows to 8192 on clusters of four: 58 us, of which about 20 find the rows and 38 move 198 MB in rows of 256 bytes
-// (5.2 TB/s).  Two launches, the second moving the rows from the whole GPU, took 14.8 and 62 us, 2 to 3 us more outside a
-// graph, and were faster only where few heads leave SMs idle (8 heads of 32768 rows: 40.6 against 43.5).  64 registers,
-// so that 512-thread blocks share an SM in pairs: 22 us for the 256 heads without.
+// 256 heads of 2064 rows, 16 moves each: 10.5 us, bound by a dozen block-wide steps.  32 heads of 32768 rows to 8192 on
+// clusters of four: 56.8 us, of which about 19 find the rows and 38 move 198 MB in rows of 256 bytes (5.2 TB/s); half
+// the warps moving: 71 us.  Two launches, the second moving the rows from the whole GPU, took 14.8 and 62 us, 2 to 3 us
+// more outside a graph, and were faster only where few heads leave SMs idle (8 heads of 32768 rows: 40.6 against 43.5).
+// 64 registers, so that 512-thread blocks share an SM in pairs: 22 us for the 256 heads without.
 #pragma once
 
 #include <cstdint>
@@ -83,6 +83,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
     extern __shared__ uint32_t ranks[]; // [rank_rows]
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
+    // every thread of the cluster; a cluster's barrier costs half a microsecond more than a block's (256 heads of 2064 rows on
+    // one block each: 13.0 against 10.9 us)
+    auto meet = [&]() {
+        if (blocks == 1) __syncthreads();
+        else cluster.sync();
+    };
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     for (int i = tid; i < 2 * 2048; i += THREADS) (&hist[0][0])[i] = 0;
@@ -102,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
     const bool copy = w_out != w || pos_out != pos;
     const int per = ((P + blocks - 1) / blocks + 31) / 32 * 32;  // rows of a block
     const int beg = min(me * per, P), rows = min(beg + per, P) - beg;
-    // By the cluster's last warp, which has the fewest rows to move, when all of the cluster has read the length.
+    // By one warp, when all of the cluster has read the length.
     auto head_done = [&]() {
         int before = 0;
         if (lane == 0) {
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
                 w_out[j] = __ldcg(w + j);
                 pos_out[j] = __ldcg(pos + j);
             }
-        if (me == blocks - 1 && wid == WARPS - 1) head_done();  // the length stays, so who reads it later reads the same
+        if (me == blocks - 1 && wid == WARPS / 2) head_done();  // the length stays, so who reads it later reads the same
         return;
     }
     const bool held = rows <= p.rank_rows;
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
                 if ((r >> (shift + bits)) == prefix) atomicAdd(&hist[pass & 1][(r >> shift) & mask], 1u);
             }
         }
-        cluster.sync();
+        meet();
         // bins from the largest down, BINS of them per thread: the one where the count from above reaches need
         unsigned int mine[BINS], sum = 0;
 #pragma unroll
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
             n += __popc(__ballot_sync(0xffffffffu, i + lane < rows && (rank_of(min(i + lane, rows - 1)) >> shift) == prefix));
         eq_before = warps_exclusive<WARPS>(n, wsum, &all);
         if (tid == 0) s_count[0] = all;
-        cluster.sync();
+        meet();
         for (int c = 0; c < me; ++c) eq_before += *cluster.map_shared_rank(&s_count[0], c);
     }
     // whether row i stays; `eqs` counts the rows at the threshold on the way
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
         s_count[1] = all_holes;
         s_count[2] = all_movers;
     }
-    cluster.sync();
+    meet();
     int moves = 0;
     for (int c = 0; c < blocks; ++c) {
         const int* n = cluster.map_shared_rank(&s_count[0], c);
@@ -270,26 +276,34 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
         if (in && !low && stay) mover_list[movers + __popc(m & ahead)] = j;
         holes += __popc(h), movers += __popc(m);
     }
-    cluster.sync();  // the lists are written; movers and holes are equally many
-    for (int i = me * THREADS + tid; i < moves; i += blocks * THREADS) {
+    meet();  // the lists are written; movers and holes are equally many
+    // Where there are few moves the first warps have their rows, the last their weights, one between the lengths.
+    for (int i = (blocks - me) * THREADS - 1 - tid; i < moves; i += blocks * THREADS) {
         const int s = __ldcg(mover_list + i), d = __ldcg(hole_list + i);
         w_out[d] = __ldcg(w + s);
         pos_out[d] = __ldcg(pos + s);
     }
-    if (me == blocks - 1 && wid == WARPS - 1) head_done();
+    if (me == blocks - 1 && wid == WARPS / 2) head_done();
     const uint4* const src[2] = {p.pool[0], p.pool[1]};
+    const int first = (me * WARPS + wid) * 8, round = blocks * WARPS * 8;
+    // lane l < 8: the rows that row l of a round comes from and goes to, read a round ahead
+    int s = -1, d = -1;
+    auto listed = [&](int m) {
+        s = d = -1;
+        if (lane < 8 && m + lane < moves) s = __ldcg(mover_list + m + lane), d = __ldcg(hole_list + m + lane);
+    };
+    listed(first);
 #pragma unroll 1
-    for (int m0 = (me * WARPS + wid) * 8; m0 < moves; m0 += blocks * WARPS * 8) {
-        // lane l < 8: where row l comes from and goes to
+    for (int m0 = first; m0 < moves; m0 += round) {
         uint32_t from = kNoRow, to = kNoRow;
-        if (lane < 8 && m0 + lane < moves) {
-            const int s = __ldcg(mover_list + m0 + lane), d = __ldcg(hole_list + m0 + lane);
+        if (d >= 0) {
             int s_in, d_in;
             const int s_e = p.pages.entry(b, s, s_in), d_e = p.pages.entry(b, d, d_in);  // both loads before a look at either
             const int s_pg = p.pages.page(s_e), d_pg = p.pages.page(d_e);
             if (s_pg >= 0) from = static_cast<uint32_t>((static_cast<long long>(s_pg) * Hkv + h) * p.pages.page_rows + s_in);
             if (d_pg >= 0) to = static_cast<uint32_t>((static_cast<long long>(d_pg) * Hkv + h) * p.pages.page_rows + d_in);
         }
+        listed(m0 + round);
         copy_rows8<VPR>(src, p.pool, from, to);
     }
 }
