@@ -956,6 +956,10 @@ PageView page_view(const e2d2_pages& pg, const e2d2_dims& dims, const DeviceInfo
     v.page_rows = pg.page_rows;
     v.max_pages = pg.max_pages;
     v.kv_heads = dims.kv_heads;
+    int l = 2;
+    while ((1ll << l) < pg.page_rows) ++l;
+    v.div_mul = static_cast<unsigned>(((1ll << (30 + l)) + pg.page_rows - 1) / pg.page_rows);
+    v.div_shift = l - 2;
     v.err = di->err;
     return v;
 }

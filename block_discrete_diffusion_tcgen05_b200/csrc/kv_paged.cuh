@@ -24,6 +24,10 @@ struct PageView {
     const int* table;  // [batch][max_pages], null: entry b is page b
     int num_pages, page_rows, max_pages;
     int kv_heads;
+    // r / page_rows for r < 2^30 as a product: with 2^l the power of two from page_rows on, div_mul = ceil(2^(30+l) / page_rows),
+    // whose excess over the quotient, less than 2^l / page_rows, moves r div_mul / 2^(30+l) by less than 1 / page_rows.
+    // (The division is some twenty instructions; every key of the softmax looks its page up.)
+    unsigned div_mul, div_shift;  // div_shift = l - 2
     unsigned int* err;
 
     __device__ __forceinline__ int capacity() const { return max_pages * page_rows; }
@@ -33,7 +37,7 @@ struct PageView {
     __device__ __forceinline__ int entry(int b, int r, int& in_page) const {
         in_page = r;
         if (table == nullptr) return b;
-        const int at = static_cast<unsigned>(r) / static_cast<unsigned>(page_rows);
+        const int at = __umulhi(static_cast<unsigned>(r), div_mul) >> div_shift;
         in_page = r - at * page_rows;
         return __ldcg(table + static_cast<size_t>(b) * max_pages + at);
     }

@@ -8,9 +8,10 @@
 // P and R are the two bf16 that hold a probability to 16 bits and more: the remainders are N more columns of the same
 // product, added to the others' when the unit ends.  A tile's softmax is that of 128 threads for every 16 columns
 // (thread = key) and the tensor cores work beside it.  HBM bounds it: 32 single tokens over up to 8192 rows take 93 us
-// (5.7 TB/s, 87 % of the copy rate), 32 blocks of 16 tokens over 2048 rows with 32 query rows per head 51 us
-// (5.4 TB/s); with 64 query rows (4 blocks over 32768 rows: 105 us, 5.0 TB/s) the softmax's 64 columns come close to
-// HBM's pace.  Short calls are a chain of latencies: one token over 500 rows takes 9.4 us.
+// (5.7 TB/s, 87 % of the copy rate), 32 blocks of 16 tokens over 2048 rows with 32 query rows per head 50 us
+// (5.5 TB/s); with 64 query rows (4 blocks over 32768 rows: 105 us, 5.0 TB/s) the softmax's 64 columns come close to
+// HBM's pace, and follow the SM's clock: 116 us once a stretch of such calls has drawn it down.  Short calls are a chain
+// of latencies: one token over 500 rows takes 9.2 us.
 //
 // A column's running maximum is shared by its warpgroup's 128 keys: each tile the threads vote whether any key beats
 // any of their columns' by more than 2^8, and only then are they reduced and O^T rescaled.  It is held negated and in
@@ -37,6 +38,8 @@ struct TcCfg {
     static constexpr int NH = 16;                     // columns per softmax warpgroup
     static constexpr int WGS = N / NH, SOFT = 128 * WGS;  // warpgroups, their threads
     static constexpr int THREADS = 128 + SOFT;        // and four control warps
+    // 640 threads start with 96 registers each: 128 x 64 and 512 x 104 are the same 61440 (without: 112 us for 105)
+    static constexpr bool SPLIT_REGS = N == 64;
     static constexpr int KV = kTcKeys * D * 2;        // K (or V) of a tile: two column halves of 128-byte rows
     static constexpr int HALF = kTcKeys * 128;
     static constexpr int Q_BYTES = N * D * 2;
@@ -60,6 +63,22 @@ struct TcCfg {
     static constexpr int ALLOC = OFF_INV + N * 4 + 1024;                  // + alignment slack
     static_assert(ALLOC <= 232448 && TMEM_COLS <= 512, "shared and tensor memory");
 };
+
+// a * b + c and a + b of pairs of floats, each pair one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+    asm("{\n\t.reg .b64 a, d;\n\t"
+        "mov.b64 d, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\t"
+        "add.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
+}
 
 // Named barrier of n threads that also says whether any of them brought true.
 __device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t n, bool mine) {
@@ -145,6 +164,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
 
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- loads: warp 0 Q and K, warp 2 V
+        if constexpr (C::SPLIT_REGS) ptx::setmaxnreg_dec<64>();
         if (delayed) test_producer_delay();
         const bool is_k = warp == 0;
         const int NS = is_k ? C::NK : C::NV;
@@ -212,6 +232,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
         if (is_k && units > 0) wait_bar_warp(q_full, (units - 1) & 1, &no_abort, p.err, true);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- S^T = K Q^T
+        if constexpr (C::SPLIT_REGS) ptx::setmaxnreg_dec<64>();
         const bool leader = ptx::elect_one();
         const uint32_t sQ = ptx::smem_u32(smem + C::OFF_Q), sK = ptx::smem_u32(smem + C::OFF_K);
         const uint64_t desc = ptx::smem_desc(0, 16, 1024, 2u);  // K (A) and Q (B): K-major, 128-byte swizzle
@@ -253,6 +274,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
         ptx::tmem_dealloc(tmem, C::TMEM_COLS);
     } else if (warp == 3) {
         // ---------------------------------------------------------------- O^T += V^T [P^T | R^T]
+        if constexpr (C::SPLIT_REGS) ptx::setmaxnreg_dec<64>();
         const bool leader = ptx::elect_one();
         const uint32_t sP = ptx::smem_u32(smem + C::OFF_P), sV = ptx::smem_u32(smem + C::OFF_V);
         const uint64_t desc = ptx::smem_desc(0, C::HALF, 1024, 2u);  // both MN-major: V^T (d contiguous), P^T (columns)
@@ -289,6 +311,7 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
     } else {
         // ---------------------------------------------------------------- softmax: thread = key lane, warpgroup = columns
         // Waits never break the loops: every warp takes every named barrier.
+        if constexpr (C::SPLIT_REGS) ptx::setmaxnreg_inc<104>();
         const int g = (warp - 4) >> 2, w = warp & 3, key = 32 * w + lane, tid = threadIdx.x - 128;
         const uint32_t lane_off = static_cast<uint32_t>(32 * w) << 16;
         const uint32_t o_tmem = tmem + lane_off + 2 * N + g * NH;  // these columns' probabilities; remainders N columns on
@@ -318,25 +341,38 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 if (key_ok && !is_own) key_ok = p.pages.page(e) >= 0;
                 wait_stage_warp(&s_full[sb], (tc >> 1) & 1, abort_flag, p.err);
                 ptx::tc_fence_after();
+                // x = a key's scores, then the exponents scale x - m.  The scores are read again where a maximum moves.
                 float x[NH];
-                {
+                auto scores = [&]() {
                     uint32_t raw[NH];
                     ptx::tmem_ld16(tmem + sb * N + lane_off + g * NH, raw);
                     ptx::tmem_wait_ld();
                     ptx::reg_fence<NH>(raw);
 #pragma unroll
                     for (int j = 0; j < NH; ++j) x[j] = __uint_as_float(raw[j]);
-                }
-                ptx::tc_fence_before();
-                mbar_arrive_warp(&s_free[sb], lane);  // the next S^T product may overwrite the buffer
-                if (!key_ok)
+                };
+                auto exponents = [&]() {
 #pragma unroll
-                    for (int j = 0; j < NH; ++j) x[j] = -INFINITY;
+                    for (int j = 0; j < NH; j += 2)
+                        fma2(x[j], x[j + 1], x[j], x[j + 1], p.scale_log2, neg_m[j], neg_m[j + 1]);
+                };
+                auto mask = [&]() {
+                    if (!__all_sync(0xffffffffu, key_ok)) {
+                        if (!key_ok)
+#pragma unroll
+                            for (int j = 0; j < NH; ++j) x[j] = -INFINITY;
+                    }
+                };
+                scores();
+                exponents();
+                mask();
                 float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < NH; ++j) top = fmaxf(top, fmaf(x[j], p.scale_log2, neg_m[j]));
+                for (int j = 0; j < NH; j += 2) top = ptx::fmax3(top, x[j], x[j + 1]);
                 if (barrier_any(1 + g, 128, top > kRescaleThreshold)) {
                     // new maxima, of every column whose keys reach past the old one
+                    scores();
+                    mask();
                     float tmp[NH];
 #pragma unroll
                     for (int j = 0; j < NH; ++j) tmp[j] = x[j] * p.scale_log2;
@@ -374,18 +410,22 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                         }
                     }
                     if (i > 0) ptx::tmem_wait_st();
+                    exponents();
+                    mask();
                 }
+                ptx::tc_fence_before();
+                mbar_arrive_warp(&s_free[sb], lane);  // the next S^T product may overwrite the buffer
                 // this key's row of [P^T | R^T]: exp2(x - m) as bf16 and bf16 remainder
                 uint32_t hi[NH / 2], lo[NH / 2];
 #pragma unroll
                 for (int j = 0; j < NH; j += 2) {
-                    const float e0 = ptx::ex2(fmaf(x[j], p.scale_log2, neg_m[j]));
-                    const float e1 = ptx::ex2(fmaf(x[j + 1], p.scale_log2, neg_m[j + 1]));
-                    l_part[j] += e0;
-                    l_part[j + 1] += e1;
+                    const float e0 = ptx::ex2(x[j]), e1 = ptx::ex2(x[j + 1]);
+                    add2(l_part[j], l_part[j + 1], e0, e1);
                     const uint32_t h2 = ptx::pack_bf16x2(e0, e1);
                     hi[j / 2] = h2;
-                    lo[j / 2] = ptx::pack_bf16x2(e0 - __uint_as_float(h2 << 16), e1 - __uint_as_float(h2 & 0xffff0000u));
+                    float r0, r1;  // e - value, exact
+                    fma2(r0, r1, __uint_as_float(h2 << 16), __uint_as_float(h2 & 0xffff0000u), -1.f, e0, e1);
+                    lo[j / 2] = ptx::pack_bf16x2(r0, r1);
                 }
                 // the buffer was read by the product of the tile before last
                 wait_stage_warp(&pv_done[sb], ((tc >> 1) & 1) ^ 1, abort_flag, p.err);
