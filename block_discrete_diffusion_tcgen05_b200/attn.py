@@ -530,7 +530,7 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
     lib = _lib.load()
     _need(k_pages, "k_pages")
     _need(v_pages, "v_pages")
-    _need(weight, "weight", dtype=torch.float32, ndim=3)
+    _need(weight, "weight", _F32, 3)
     B, Hkv, d = weight.shape[0], k_pages.shape[1], k_pages.shape[3]
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
@@ -541,7 +541,8 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
     pos_out = pos if pos_out is None else pos_out
     P_out = P if P_out is None else P_out
     rows = (B, Hkv, cap)
-    _need_rows(weight, "weight", rows, _F32)
+    if weight.shape != rows:
+        raise ValueError(f"weight must be [B, Hkv, row capacity] = {rows}, got {tuple(weight.shape)}")
     _need_rows(pos, "pos", rows, _I32)
     if weight_out is not weight:
         _need_rows(weight_out, "weight_out", rows, _F32)
@@ -553,7 +554,7 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
     st = lib.e2d2_kv_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), pages, P.data_ptr(), weight.data_ptr(),
                                  pos.data_ptr(), tokens.data_ptr(), int(keep), int(recent), weight_out.data_ptr(),
                                  pos_out.data_ptr(), P_out.data_ptr(), _dims(B, Hkv, Hkv, d, None), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _stream(k_pages))
+                                 ws.nbytes, _stream(k_pages))
     _lib.check(st, "e2d2_kv_cache_evict")
     return P_out
 
