@@ -26,6 +26,7 @@
 
 #include <cooperative_groups.h>
 
+#include "evict_select.cuh"
 #include "kv_paged.cuh"
 
 namespace e2d2 {
@@ -75,10 +76,10 @@ __device__ __forceinline__ int warps_exclusive(int x, int* wsum, int* total) {
 template <int THREADS, int VPR>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const __grid_constant__ EvictParams p) {
     namespace cg = cooperative_groups;
-    constexpr int WARPS = THREADS / 32, BINS = 2048 / THREADS, BATCH = 8;
-    __shared__ __align__(16) unsigned int hist[2][2048];
+    constexpr int WARPS = THREADS / 32, BINS = kEvictBins / THREADS, BATCH = 8;
+    __shared__ __align__(16) unsigned int hist[2][kEvictBins];
     __shared__ int wsum[WARPS];
-    __shared__ unsigned int s_pick[3];  // leading bits, rows of them that stay, rows that have them
+    __shared__ EvictPick s_pick;
     __shared__ int s_count[3];          // this block's rows at the threshold, holes, movers
     extern __shared__ uint32_t ranks[]; // [rank_rows]
     cg::cluster_group cluster = cg::this_cluster();
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
     };
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    for (int i = tid; i < 2 * 2048; i += THREADS) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 2 * kEvictBins; i += THREADS) (&hist[0][0])[i] = 0;
     ptx::griddep_wait();
     const int unit = blockIdx.x / blocks, Hkv = p.pages.kv_heads, cap = p.pages.capacity();
     const int b = unit / Hkv, h = unit - b * Hkv;
@@ -120,13 +121,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
         for (int e = lane; e < p.batch; e += 32) p.P_out[e] = min(ragged_clamp(__ldcg(p.P_dev + e), cap), p.keep);
         if (lane == 0) *p.heads_done = 0;
     };
-    if (P <= p.keep) {  // the same for every block of the cluster
+    // The same for every block of the cluster: one that reads the length after head_done() has let it be written finds
+    // min(P, keep), for which this holds too.
+    if (!evict_selects(P, p.keep)) {
         if (copy)
-            for (int j = beg + tid; j < beg + rows; j += THREADS) {
+            for (int j = beg + tid; j < min(beg + rows, p.keep); j += THREADS) {
                 w_out[j] = __ldcg(w + j);
                 pos_out[j] = __ldcg(pos + j);
             }
-        if (me == blocks - 1 && wid == WARPS / 2) head_done();  // the length stays, so who reads it later reads the same
+        if (me == blocks - 1 && wid == WARPS / 2) head_done();
         return;
     }
     const bool held = rows <= p.rank_rows;
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
     // The keep-th largest rank, 11, 11 and 10 bits a pass: prefix = its leading bits, need = how many rows with that
     // prefix stay; done when all of them do.
     unsigned int prefix = 0, need = p.keep, equal = 0;
-    int shift = 21, bits = 11;
+    int shift = evict_pass_shift(0), bits = evict_pass_bits(0);
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
         if (pass > 0) {
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
 #pragma unroll
         for (int i = 0; i < BINS; ++i) mine[i] = 0;
         for (int c = 0; c < blocks; ++c) {
-            const unsigned int* h = cluster.map_shared_rank(&hist[pass & 1][0], c) + 2048 - BINS * (tid + 1);
+            const unsigned int* h = cluster.map_shared_rank(&hist[pass & 1][0], c) + kEvictBins - BINS * (tid + 1);
             if constexpr (BINS % 4 == 0) {
 #pragma unroll
                 for (int i = 0; i < BINS; i += 4) {
@@ -198,22 +201,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
         unsigned int above = warps_exclusive<WARPS>(static_cast<int>(__shfl_sync(0xffffffffu, inc, 31)), wsum, &all) + inc - sum;
         // every block has read the other histogram (the cluster has met since): it is clear for the pass after next
         if (pass == 1)
-            for (int i = tid; i < 2048; i += THREADS) hist[0][i] = 0;
-        // need = 0 (keep = 0): the first thread takes its first bin, and nothing of it stays
-        if (need == 0 ? tid == 0 : (above < need && need <= above + sum)) {
-            int i = 0;
-            while (i < BINS - 1 && above + mine[i] < need) above += mine[i++];
-            s_pick[0] = (prefix << bits) | ((2047u - BINS * tid - i) & ((1u << bits) - 1u));
-            s_pick[1] = need == 0 ? 0 : need - above;
-            s_pick[2] = mine[i];
-        }
+            for (int i = tid; i < kEvictBins; i += THREADS) hist[0][i] = 0;
+        EvictPick next;
+        if (evict_pick<BINS>(mine, above, sum, need, tid, bits, prefix, next)) s_pick = next;
         __syncthreads();
-        prefix = s_pick[0];
-        need = s_pick[1];
-        equal = s_pick[2];
+        prefix = s_pick.prefix;
+        need = s_pick.need;
+        equal = s_pick.equal;
         if (need == equal || shift == 0) break;
-        bits = pass == 0 ? 11 : 10;
-        shift -= bits;
+        bits = evict_pass_bits(pass + 1);
+        shift = evict_pass_shift(pass + 1);
     }
     // Rows above the threshold stay, and the first `need` of the `equal` rows at it.  A warp takes a run of the
     // block's rows, 32 at a time, in their order.

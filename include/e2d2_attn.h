@@ -392,7 +392,8 @@ E2D2_API e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d
  * weight counts as below every number, -0 as 0.  Kept rows below `keep` stay where they are, and
  * the i-th kept row at or past `keep` moves, K, V, weight and position, to the i-th row below
  * `keep` that is not kept.  Attention does not depend on the order of the cached rows; pos keeps
- * each row's token.  Entries of at most `keep` rows stay as they are.
+ * each row's token.  Entries of at most `keep` rows stay as they are; keep = 0 empties every entry, protected rows
+ * too.
  *   weight_out, pos_out: rows below min(P, keep) written, the others not; each is its input (in
  *   place) or does not overlap it.  P_out [batch]: min(P, keep); may be P_dev.  Cache rows at or
  *   past P_out[b] keep their bits and need not be kept.

@@ -1,0 +1,144 @@
+"""GPU tests of the paged-cache calls at their edges: budgets of nothing, and what each call must leave alone.  Every
+buffer that a call may write lies inside a larger one whose margins are checked afterwards, the workspace too."""
+import numpy as np
+import pytest
+import torch
+
+from block_discrete_diffusion_tcgen05_b200 import attn
+
+pytestmark = pytest.mark.gpu
+
+PAD = 8192
+
+
+class Guarded:
+    """Tensors with margins of one byte value on either side; check() says whether any margin changed."""
+
+    def __init__(self, fill=0xA5):
+        self.fill, self.held = fill, []
+
+    def __call__(self, t):
+        n = t.numel() * t.element_size()
+        big = torch.full((n + 2 * PAD,), self.fill, dtype=torch.uint8, device="cuda")
+        inner = big[PAD:PAD + n].view(t.dtype).view(t.shape)
+        inner.copy_(t)
+        self.held.append((big, n))
+        return inner
+
+    def check(self):
+        for i, (big, n) in enumerate(self.held):
+            assert (big[:PAD] == self.fill).all() and (big[PAD + n:] == self.fill).all(), f"buffer {i}: written outside"
+
+
+def raw(t):
+    return t.view(torch.int16)
+
+
+def kept_rows(w, pos, protect, keep):
+    """Rows that stay by the definition, as a mask: w, pos numpy [P]."""
+    P = len(w)
+    kind = np.where(pos >= protect, 2, np.where(np.isnan(w), 0, 1))
+    value = np.where(kind == 1, np.where(np.isnan(w), 0, w), 0).astype(np.float64)
+    order = np.lexsort((np.arange(P), -value, -kind))
+    mask = np.zeros(P, bool)
+    mask[order[:keep]] = True
+    return mask
+
+
+def run_evict(P, keep, recent=0, d=64, page=16, Hkv=3, capacity=None, seed=1, in_place=True, weight=None, tokens=None,
+              pos=None, bad=(), dirty=False):
+    """One eviction of random pools against the definition, bit by bit.  weight: [B][Hkv][capacity] numpy or a function of
+    (rng, shape); tokens: one per entry, default P; bad: (entry, page of it) pairs whose table entry names no page;
+    dirty: the lists of the workspace hold row numbers past every cache, as a call of other sizes may leave them."""
+    B = len(P)
+    rng = np.random.default_rng(seed)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    rows = capacity or max(max(P), 1)
+    each = -(-rows // page) if page else 1
+    cap = each * page if page else rows
+    table_h = np.arange(B).reshape(B, 1) if not page else rng.permutation(B * each + 2)[:B * each].reshape(B, each)
+    n_pages, per = (B, cap) if not page else (B * each + 2, page)
+    guard = Guarded()
+    k0, v0 = (torch.randint(-2 ** 15, 2 ** 15, (n_pages, Hkv, per, d), dtype=torch.int16, device="cuda", generator=g)
+              .view(torch.bfloat16) for _ in range(2))
+    k, v = guard(raw(k0)).view(torch.bfloat16), guard(raw(v0)).view(torch.bfloat16)
+    shape = (B, Hkv, cap)
+    w0 = np.exp(2 * rng.standard_normal(shape)) if weight is None else (weight(rng, shape) if callable(weight) else weight)
+    w0 = np.ascontiguousarray(w0, np.float32)
+    if pos is None:
+        pos = np.zeros(shape, np.int32)
+        for b in range(B):
+            for h in range(Hkv):
+                pos[b, h, :P[b]] = rng.permutation(P[b])
+    tokens = list(P) if tokens is None else tokens
+    table = None
+    if page:
+        named = table_h.astype(np.int32)
+        for b, i in bad:
+            named[b, i] = n_pages + 5
+        table = torch.from_numpy(named).cuda()
+    wd, pd = guard(torch.from_numpy(w0).cuda()), guard(torch.from_numpy(pos).cuda())
+    Pd, td = guard(torch.tensor(P, dtype=torch.int32, device="cuda")), torch.tensor(tokens, dtype=torch.int32, device="cuda")
+    wo, po, Po = (wd, pd, Pd) if in_place else (guard(torch.full_like(wd, -5.0)), guard(torch.full_like(pd, -5)),
+                                                guard(torch.full_like(Pd, -5)))
+    was_w, was_p = wo.cpu().numpy().copy(), po.cpu().numpy().copy()
+    ws = torch.zeros(attn.evict_workspace_bytes(B, Hkv, cap), dtype=torch.uint8, device="cuda")
+    if dirty:
+        ws[16:].view(torch.int32).fill_(1 << 24)
+    ws = guard(ws)
+    attn.kv_cache_evict(k, v, table, Pd, wd, pd, td, keep, recent=recent, weight_out=wo, pos_out=po, P_out=Po, workspace=ws)
+    torch.cuda.synchronize()
+    error = attn.last_device_error()
+    guard.check()
+    assert ws[:16].eq(0).all(), "the workspace is not reusable"
+    assert Po.tolist() == [min(p, keep) for p in P]
+    moved = 0
+    src, dst, head = [], [], []
+    got_w, got_p = wo.cpu().numpy(), po.cpu().numpy()
+    for b in range(B):
+        n, lost = P[b], {i for e, i in bad if e == b}
+        m = min(n, keep)
+        for h in range(Hkv):
+            want_w, want_p = was_w[b, h].copy(), was_p[b, h].copy()
+            want_w[:m], want_p[:m] = w0[b, h, :m], pos[b, h, :m]
+            if n > keep:
+                mask = kept_rows(w0[b, h, :n], pos[b, h, :n], tokens[b] - recent, keep)
+                holes, movers = np.flatnonzero(~mask[:keep]), keep + np.flatnonzero(mask[keep:])
+                assert len(holes) == len(movers)
+                if page:  # a move whose source or target no page backs is not made
+                    ok = ~(np.isin(holes // page, list(lost)) | np.isin(movers // page, list(lost)))
+                    holes, movers = holes[ok], movers[ok]
+                want_w[holes], want_p[holes] = w0[b, h, movers], pos[b, h, movers]
+                moved += len(holes)
+                src += [(table_h[b, s // per], s % per) for s in movers]
+                dst += [(table_h[b, t // per], t % per) for t in holes]
+                head += [h] * len(holes)
+            assert np.array_equal(got_w[b, h], want_w, equal_nan=True), (b, h)
+            assert np.array_equal(got_p[b, h], want_p), (b, h)
+    if moved:
+        s, t = (torch.tensor(np.array(x), device="cuda") for x in (src, dst))
+        hd = torch.tensor(head, device="cuda")
+        for x in (k0, v0):
+            raw(x)[t[:, 0], hd, t[:, 1]] = raw(x)[s[:, 0], hd, s[:, 1]]
+    assert torch.equal(raw(k), raw(k0)) and torch.equal(raw(v), raw(v0))
+    return moved, error
+
+
+# ------------------------------------------------------------------------------------- a budget of nothing
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("tokens", ["none", "some", "all"])
+@pytest.mark.parametrize("P,page,d,Hkv", [([300], 16, 64, 3), ([300, 17, 0, 64], 48, 32, 2), ([1], 16, 128, 1),
+                                          ([9000], 0, 64, 1), ([33], 0, 128, 5)])
+def test_a_budget_of_nothing_evicts_everything(P, page, d, Hkv, tokens, in_place):
+    """keep = 0 with no, some or all of the positions at or past `tokens` (protected, but for the budget): the lengths
+    become 0, and not a row, weight or position is written, whatever the workspace's lists hold."""
+    tok = {"none": P, "some": [p // 2 for p in P], "all": [0] * len(P)}[tokens]
+    assert run_evict(P, 0, d=d, page=page, Hkv=Hkv, tokens=tok, in_place=in_place, dirty=True, seed=11) == (0, 0)
+
+
+@pytest.mark.parametrize("keep", [1, 2, 149])
+def test_protected_rows_past_a_small_budget(keep):
+    """As many protected rows as there are, and room for a few of them: the lowest stay."""
+    moved, error = run_evict([300, 40], keep, tokens=[0, 20], dirty=True, seed=12)
+    assert error == 0
