@@ -321,18 +321,17 @@ __global__ void __launch_bounds__(kWeighThreads, WeighCfg<D, N>::CTAS) kv_weigh_
             if (unit != have) {
                 have = unit;
                 __syncwarp();  // the last unit's values have been read
-                for (int c = lane; c < n16; c += 32) {
-                    const float x = c < p.n ? __ldcg(p.lse + static_cast<long long>(have) * p.rows + p.row0 + c) : -INFINITY;
-                    lse2[c] = x == -INFINITY ? INFINITY : x * 1.4426950408889634f;  // such a row adds nothing
-                }
+                // -infinity: the column adds nothing, whatever its scores are -- a row that saw nothing (its query may be
+                // anything, NaN included), and the columns past the last row, which hold another unit's query, or none,
+                // or (past n16) old scores
+                for (int c = lane; c < (n16 + 31) / 32 * 32; c += 32)
+                    lse2[c] = c < p.n ? __ldcg(p.lse + static_cast<long long>(have) * p.rows + p.row0 + c) * 1.4426950408889634f : -INFINITY;
                 __syncwarp();
             }
             if (!wait_stage_warp(&s_full[g], use & 1, abort_flag, p.err)) break;
             ptx::tc_fence_after();
             float sum = 0.f;
             for (int c0 = 0; c0 < n16; c0 += 32) {
-                // columns past the last row hold another unit's query, or none, or (past n16) old scores: they add
-                // nothing whatever they are
                 uint32_t raw[32];
                 const uint32_t ta = tmem + g * N + (static_cast<uint32_t>(32 * w) << 16) + c0;
                 ptx::tmem_ld32(ta, raw);
@@ -341,8 +340,8 @@ __global__ void __launch_bounds__(kWeighThreads, WeighCfg<D, N>::CTAS) kv_weigh_
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float e = ptx::ex2(__uint_as_float(raw[c]) * p.scale_log2 - lse2[c0 + c]);
-                    part[c & 3] += c0 + c < p.n ? e : 0.f;
+                    const float z = lse2[c0 + c], e = ptx::ex2(__uint_as_float(raw[c]) * p.scale_log2 - z);
+                    part[c & 3] += z == -INFINITY ? 0.f : e;
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
             }

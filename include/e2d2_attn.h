@@ -378,7 +378,7 @@ E2D2_API e2d2_status e2d2_kv_cache_append_paged(void* k_pages, void* v_pages, e2
  * over the G * S query rows i that read kv head h; rows at or past P_dev[b] are not written.
  *   q [batch][q_heads][S][d] and lse [batch][q_heads][S]: the queries and the log-sum-exp of an
  *   attention call (which may have seen more rows than these); a row with lse = -infinity adds
- *   nothing.  weight_out is weight itself (in place) or does not overlap it.  No atomics: two calls
+ *   nothing, whatever its query holds.  weight_out is weight itself (in place) or does not overlap it.  No atomics: two calls
  *   with the same inputs give the same bits.
  */
 E2D2_API e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d2_pages pages, const int* P_dev,

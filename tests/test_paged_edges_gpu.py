@@ -142,3 +142,30 @@ def test_protected_rows_past_a_small_budget(keep):
     """As many protected rows as there are, and room for a few of them: the lowest stay."""
     moved, error = run_evict([300, 40], keep, tokens=[0, 20], dirty=True, seed=12)
     assert error == 0
+
+
+# --------------------------------------------------------------------------- query rows that saw nothing
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("d,Hq,Hkv,S", [(128, 4, 4, 1), (128, 4, 2, 16), (128, 8, 2, 16), (64, 4, 2, 5), (32, 4, 2, 40),
+                                        (64, 8, 1, 33)])
+def test_a_query_row_that_saw_nothing_adds_nothing_whatever_it_holds(d, Hq, Hkv, S, value):
+    """lse = -infinity: the row is padding, its query may hold anything.  The weights are those with any other query in
+    its place, bit by bit."""
+    B, cap = 3, 400
+    g = torch.Generator(device="cuda")
+    g.manual_seed(21)
+    k = torch.randn(B, Hkv, cap, d, device="cuda", generator=g).bfloat16()
+    q = torch.randn(B, Hq, S, d, device="cuda", generator=g).bfloat16()
+    P = torch.tensor([400, 0, 131], dtype=torch.int32, device="cuda")
+    lse = torch.full((B, Hq, S), 4.0, device="cuda")
+    nothing = torch.zeros(B, Hq, S, dtype=torch.bool, device="cuda")
+    nothing[0, ::2, S // 2], nothing[0, -1, -1], nothing[2] = True, True, True   # rows here and there, and an entry of padding
+    lse[nothing] = float("-inf")
+    w0 = torch.rand(B, Hkv, cap, device="cuda", generator=g)
+    plain = attn.kv_cache_weigh(q, k, None, P, lse, w0, out=torch.zeros_like(w0))
+    q[nothing] = value
+    out = attn.kv_cache_weigh(q, k, None, P, lse, w0, out=torch.zeros_like(w0))
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain) and torch.isfinite(out).all()
+    assert torch.equal(out[2, :, :131], w0[2, :, :131])
+    assert attn.last_device_error() == 0
