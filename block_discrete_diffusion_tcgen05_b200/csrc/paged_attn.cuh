@@ -564,8 +564,10 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                             for (int y = 0; y < NT; ++y) o[y][2 * r] *= f, o[y][2 * r + 1] *= f;
                         }
                     }
-                    // P = exp2(S - m), as bf16 plus bf16 remainder: the first product's accumulators are the
-                    // second's A fragments
+                    // P = exp2(S - m), as bf16 plus bf16 remainder: the first product's accumulators are the second's A
+                    // fragments.  The bf16 is the largest below the probability, so that the remainder has its sign
+                    // (at most 2^-7 of it, rounded to within 2^-16): an infinite V row gives infinity, where a remainder
+                    // of zero or below gives NaN.
                     const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
                     uint32_t ph[SUB][4], pl[SUB][4];
 #pragma unroll
@@ -576,7 +578,8 @@ __global__ void __launch_bounds__(PagedCfg<D, RW>::THREADS, PagedCfg<D, RW>::CTA
                             const float mm = (e & 1) ? m1 : m0;
                             const float p0 = ptx::ex2(x[0] * p.scale_log2 - mm), p1 = ptx::ex2(x[1] * p.scale_log2 - mm);
                             l[e & 1] += p0 + p1;
-                            const uint32_t hi = ptx::pack_bf16x2(p0, p1);
+                            constexpr float below = 1.f - 0x1p-23f;
+                            const uint32_t hi = __byte_perm(__float_as_uint(p0 * below), __float_as_uint(p1 * below), 0x7632);
                             ph[sb][e] = hi;
                             pl[sb][e] = ptx::pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
                         }

@@ -507,7 +507,8 @@ __global__ void __launch_bounds__(TcCfg<N>::THREADS, 1) paged_attn_tc_kernel(con
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float o = __uint_as_float(oh[k]) + __uint_as_float(ol[k]);
+                    // an infinite value's products: infinite with the probabilities, anything with the remainders
+                    const float hi = __uint_as_float(oh[k]), o = fabsf(hi) == INFINITY ? hi : hi + __uint_as_float(ol[k]);
                     if (whole) {
                         if (c8 + k < cols) out[(c8 + k) * D] = __float2bfloat16_rn(walk.n > 0 ? o * inv_l[c8 + k] : 0.f);
                     } else if (c8 + k < cols) {

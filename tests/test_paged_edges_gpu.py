@@ -169,3 +169,32 @@ def test_a_query_row_that_saw_nothing_adds_nothing_whatever_it_holds(d, Hq, Hkv,
     assert torch.equal(out, plain) and torch.isfinite(out).all()
     assert torch.equal(out[2, :, :131], w0[2, :, :131])
     assert attn.last_device_error() == 0
+
+
+# ----------------------------------------------------------------------------------- infinite values
+@pytest.mark.parametrize("d,Hq,S", [(128, 4, 1), (128, 4, 16), (128, 4, 32), (128, 4, 50), (64, 4, 1), (64, 4, 9), (64, 4, 16),
+                                    (64, 4, 40), (32, 4, 3), (32, 4, 40)])
+@pytest.mark.parametrize("P", [100, 900])
+@pytest.mark.parametrize("block", [False, True])
+def test_an_infinite_value_gives_infinity_in_its_column(d, Hq, S, P, block):
+    """Every probability is positive: a row in use whose value is infinite makes its column infinite, of both signs NaN,
+    and no other column changes a bit.  In the cached rows, and in the block's own."""
+    Hkv = 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    normal = lambda *shape: torch.randn(shape, device="cuda", generator=g).bfloat16()  # noqa: E731
+    q, k, v = normal(1, Hq, S, d), normal(1, Hkv, P, d), normal(1, Hkv, P, d)
+    kb, vb = (normal(1, Hkv, S, d), normal(1, Hkv, S, d)) if block else (None, None)
+    Pd = torch.tensor([P], dtype=torch.int32, device="cuda")
+    plain, lse0 = attn.decoder_sample_paged(q, k, v, None, Pd, kb, vb)
+    v[0, 0, 37, 5] = float("inf")
+    v[0, 0, P - 1, 9], v[0, 0, 2, 9] = -float("inf"), float("inf")
+    (v if not block else vb)[0, 1, 0, 17] = -float("inf")
+    out, lse = attn.decoder_sample_paged(q, k, v, None, Pd, kb, vb)
+    torch.cuda.synchronize()
+    a, b = out[0, :Hq // 2], out[0, Hq // 2:]
+    assert (a[..., 5] == float("inf")).all() and a[..., 9].isnan().all() and (b[..., 17] == -float("inf")).all()
+    for got, ref, touched in ((a, plain[0, :Hq // 2], (5, 9)), (b, plain[0, Hq // 2:], (17,))):
+        rest = [c for c in range(d) if c not in touched]
+        assert torch.equal(got[..., rest], ref[..., rest])
+    assert torch.equal(lse, lse0)
