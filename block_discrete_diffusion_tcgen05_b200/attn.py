@@ -405,6 +405,14 @@ def _need_rows(t, name: str, shape, dtype):
         raise ValueError(f"{name} must be [B, Hkv, row capacity] = {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _int32(x, name: str) -> int:
+    """A count for the C call: ctypes would take the low 32 bits of a larger one."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def sample_paged_workspace_bytes(batch, q_heads, kv_heads, head_dim, S) -> int:
     """Bytes of workspace a paged sampling call needs (no GPU needed)."""
     lib = _lib.load()
@@ -537,6 +545,7 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
     pages, cap = _pages(k_pages, page_table, B)
     _need_ints(P, "P", B)
     _need_ints(tokens, "tokens", B)
+    keep, recent = _int32(keep, "keep"), _int32(recent, "recent")
     weight_out = weight if weight_out is None else weight_out
     pos_out = pos if pos_out is None else pos_out
     P_out = P if P_out is None else P_out
@@ -552,7 +561,7 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
         _need_ints(P_out, "P_out", B)
     ws = evict_workspace(weight) if workspace is None else _need_workspace(workspace)
     st = lib.e2d2_kv_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), pages, P.data_ptr(), weight.data_ptr(),
-                                 pos.data_ptr(), tokens.data_ptr(), int(keep), int(recent), weight_out.data_ptr(),
+                                 pos.data_ptr(), tokens.data_ptr(), keep, recent, weight_out.data_ptr(),
                                  pos_out.data_ptr(), P_out.data_ptr(), _dims(B, Hkv, Hkv, d, None), ws.data_ptr(),
                                  ws.nbytes, _stream(k_pages))
     _lib.check(st, "e2d2_kv_cache_evict")
