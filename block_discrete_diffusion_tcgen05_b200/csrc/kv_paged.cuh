@@ -191,13 +191,12 @@ __global__ void __launch_bounds__(256, 4) kv_append_paged_kernel(const __grid_co
             const int unit = static_cast<int>(from / a.S_new), s = static_cast<int>(from - static_cast<long long>(unit) * a.S_new);
             const int b = unit / Hkv, h = unit - b * Hkv;
             const long long r = static_cast<long long>(ragged_clamp(__ldcg(a.P_dev + b), cap)) + s;
-            if (r < cap) {  // rows past the capacity are not written
-                if (a.weight != nullptr) {
-                    const long long w = static_cast<long long>(unit) * cap + r;
-                    a.weight[w] = 0.f;
-                    a.pos[w] = __ldcg(a.tokens + b) + s;
-                }
-                to = static_cast<uint32_t>(a.pages.pool_row(b, h, static_cast<int>(r)));  // -1: kNoRow
+            // rows past the capacity, and those that no page backs, are not written; nor are their weights and positions
+            if (r < cap) to = static_cast<uint32_t>(a.pages.pool_row(b, h, static_cast<int>(r)));  // -1: kNoRow
+            if (to != kNoRow && a.weight != nullptr) {
+                const long long w = static_cast<long long>(unit) * cap + r;
+                a.weight[w] = 0.f;
+                a.pos[w] = __ldcg(a.tokens + b) + s;
             }
         }
         copy_rows8<VPR>(a.src, a.pool, static_cast<uint32_t>(from), to);

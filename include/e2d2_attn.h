@@ -325,8 +325,9 @@ E2D2_API e2d2_status e2d2_kv_cache_append_ragged(void* k_cache, void* v_cache, i
  *   page_rows: a multiple of 16 (else E2D2_ERR_UNSUPPORTED).
  *   page_table == NULL: contiguous caches [batch][kv_heads][capacity][d] -- the layout of the other
  *   calls -- as one page per entry: num_pages = batch, max_pages = 1, page_rows = capacity (any).
- *   A looked-up page id outside [0, num_pages) is never followed: its rows are not written and take
- *   no part in attention, and e2d2_last_device_error() reports E2D2_ERR_PAGE.
+ *   A looked-up page id outside [0, num_pages) is never followed: its rows are not written, nor are their
+ *   weight and position by the append, they take no part in attention, their accumulated weight stays
+ *   as it is, and e2d2_last_device_error() reports E2D2_ERR_PAGE.
  *   Entries may share pages (a common prefix) as long as no call writes to a shared page.
  *   batch <= 1024, batch * kv_heads <= 65535, row capacity < 2^30, and the work in steps of 16 rows below 2^31:
  *   batch * kv_heads * ceil(G * S / 64) * ((row capacity + S) / 16 + 6) (else E2D2_ERR_SHAPE).

@@ -198,3 +198,42 @@ def test_an_infinite_value_gives_infinity_in_its_column(d, Hq, S, P, block):
         rest = [c for c in range(d) if c not in touched]
         assert torch.equal(got[..., rest], ref[..., rest])
     assert torch.equal(lse, lse0)
+
+
+# ------------------------------------------------------------------------- page ids outside the pool
+E2D2_ERR_PAGE = 10
+
+
+@pytest.mark.parametrize("bad", [-1, 11, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 48), (32, 32)])
+def test_an_append_leaves_rows_without_a_page_alone(d, page, bad):
+    """Neither K and V nor the weight and position of such a row are written; the rows around them are, and the error
+    is reported."""
+    B, Hkv, S, each = 2, 3, 2 * page + 5, 4
+    cap, pages = each * page, 11
+    rng = np.random.default_rng(41)
+    table_h = rng.permutation(pages)[:B * each].reshape(B, each).astype(np.int32)
+    guard = Guarded()
+    k, v = (guard(torch.full((pages, Hkv, page, d), 3.0, dtype=torch.bfloat16, device="cuda")) for _ in range(2))
+    w, pos = guard(torch.full((B, Hkv, cap), 7.0, device="cuda")), guard(torch.full((B, Hkv, cap), -9, dtype=torch.int32, device="cuda"))
+    new = torch.arange(1, S + 1, device="cuda", dtype=torch.float32).view(1, 1, S, 1).expand(B, Hkv, S, d).bfloat16().contiguous()
+    P, tok = [7, page], [100, 5]
+    broken = torch.from_numpy(table_h.copy())
+    broken[0, 1] = bad
+    attn.kv_cache_append_paged(k, v, broken.cuda(), torch.tensor(P, dtype=torch.int32, device="cuda"), new, -new, weight=w,
+                               pos=pos, tokens=torch.tensor(tok, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert attn.last_device_error() == E2D2_ERR_PAGE and attn.last_device_error() == 0
+    guard.check()
+    want_k, want_w, want_p = torch.full((pages, Hkv, page, d), 3.0), torch.full((B, Hkv, cap), 7.0), torch.full((B, Hkv, cap), -9)
+    want_v = want_k.clone()
+    for b in range(B):
+        for i in range(S):
+            r = P[b] + i
+            if b == 0 and r // page == 1:
+                continue
+            value = new[b, 0, i, 0].float().item()
+            want_k[table_h[b, r // page], :, r % page], want_v[table_h[b, r // page], :, r % page] = value, -value
+            want_w[b, :, r], want_p[b, :, r] = 0.0, tok[b] + i
+    assert torch.equal(k.float().cpu(), want_k) and torch.equal(v.float().cpu(), want_v)
+    assert torch.equal(w.cpu(), want_w) and torch.equal(pos.cpu().long(), want_p.long())
