@@ -275,10 +275,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
     }
     meet();  // the lists are written; movers and holes are equally many
     // Where there are few moves the first warps have their rows, the last their weights, one between the lengths.
+    // (A move whose source or target no page backs is not made: the hole keeps its row, weight and position.)
     for (int i = (blocks - me) * THREADS - 1 - tid; i < moves; i += blocks * THREADS) {
         const int s = __ldcg(mover_list + i), d = __ldcg(hole_list + i);
-        w_out[d] = __ldcg(w + s);
-        pos_out[d] = __ldcg(pos + s);
+        const float wv = __ldcg(w + s);
+        const int pv = __ldcg(pos + s);
+        int in_page;
+        const int s_e = p.pages.entry(b, s, in_page), d_e = p.pages.entry(b, d, in_page);
+        if (p.pages.page(s_e) >= 0 && p.pages.page(d_e) >= 0) w_out[d] = wv, pos_out[d] = pv;
     }
     if (me == blocks - 1 && wid == WARPS / 2) head_done();
     const uint4* const src[2] = {p.pool[0], p.pool[1]};

@@ -399,6 +399,8 @@ E2D2_API e2d2_status e2d2_kv_cache_weigh(const void* q, const void* k_pages, e2d
  *   place) or does not overlap it.  P_out [batch]: min(P, keep); may be P_dev.  Cache rows at or
  *   past P_out[b] keep their bits and need not be kept.
  *   Every page of rows below P must be the entry's own (not shared).
+ *   A move from or to a row whose page id lies outside the pool is not made (E2D2_ERR_PAGE): the target keeps
+ *   its row, weight and position.
  *   workspace: at least e2d2_kv_cache_evict_workspace(dims, pages) bytes, 16-byte aligned, zero-filled
  *   once; completed calls leave it reusable by later evictions of any dims on the same stream.
  *   Calls that may run at the same time need different workspaces.

@@ -237,3 +237,12 @@ def test_an_append_leaves_rows_without_a_page_alone(d, page, bad):
             want_w[b, :, r], want_p[b, :, r] = 0.0, tok[b] + i
     assert torch.equal(k.float().cpu(), want_k) and torch.equal(v.float().cpu(), want_v)
     assert torch.equal(w.cpu(), want_w) and torch.equal(pos.cpu().long(), want_p.long())
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("d,page,bad", [(64, 16, [(0, 2)]), (128, 48, [(0, 5)]), (32, 16, [(0, 1), (0, 17), (1, 0)])])
+def test_an_eviction_makes_no_move_from_or_to_a_row_without_a_page(d, page, bad, in_place):
+    """Where the target's page or the source's is none of the pool, the hole keeps its row, weight and position: the
+    three belong together before and after."""
+    moved, error = run_evict([300, 290], 150, recent=10, d=d, page=page, bad=bad, in_place=in_place, seed=42)
+    assert moved > 0 and error == E2D2_ERR_PAGE
