@@ -1198,7 +1198,7 @@ e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const void* k_page
 e2d2_status e2d2_kv_cache_append_paged(void* k_pages, void* v_pages, e2d2_pages pages, const int* P_dev,
                                        const void* k_new, const void* v_new, int S_new, float* weight, int* pos,
                                        const int* tokens_dev, e2d2_dims dims, cudaStream_t stream) {
-    if (!k_pages || !v_pages || !P_dev || !k_new || !v_new) return E2D2_ERR_INVALID_ARG;
+    if (!k_pages || !v_pages || !P_dev || (S_new != 0 && (!k_new || !v_new))) return E2D2_ERR_INVALID_ARG;
     if (!weight != !pos || !weight != !tokens_dev) return E2D2_ERR_INVALID_ARG;
     e2d2_status s = check_dims(dims);
     if (s != E2D2_OK) return s;

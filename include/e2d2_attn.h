@@ -362,7 +362,8 @@ E2D2_API e2d2_status e2d2_attn_decoder_sample_paged(const void* q_blk, const voi
 /*
  * Append to a paged cache: as e2d2_kv_cache_append_ragged, rows P_dev[b]..P_dev[b]+S_new-1 of entry
  * b found through the page table; rows at or past the row capacity are not written, S_new above it
- * is E2D2_ERR_CAPACITY.  The pages that are written must be the entry's own.
+ * is E2D2_ERR_CAPACITY, S_new = 0 does nothing (k_new and v_new may then be NULL).  The pages that are
+ * written must be the entry's own.
  *   weight [batch][kv_heads][row capacity] float, pos the same shape int, tokens_dev DEVICE
  *   [batch] ints: all three or none.  With them the new rows' accumulated weight becomes 0 and
  *   their position tokens_dev[b] + i (tokens_dev[b]: tokens the entry has seen before the block),

@@ -1,8 +1,8 @@
-"""The paged-cache calls' arguments at their edges, without a GPU: counts that 32 bits do not hold."""
+"""The paged-cache calls' arguments at their edges, without a GPU: counts that 32 bits do not hold, blocks of no rows."""
 import pytest
 import torch
 
-from block_discrete_diffusion_tcgen05_b200 import attn
+from block_discrete_diffusion_tcgen05_b200 import _lib, attn, build
 from test_binding_marshalling_cpu import WS_BYTES, bf16, rec  # noqa: F401
 
 B, Hkv, d = 2, 2, 64
@@ -31,3 +31,17 @@ def test_the_largest_budget_is_passed_on(rec):  # noqa: F811
                         recent=2 ** 31 - 1, workspace=ws)
     c = rec.call("e2d2_kv_cache_evict")
     assert (c["keep"], c["recent"]) == (2 ** 31 - 1, 2 ** 31 - 1)
+
+
+def test_an_append_of_no_rows_does_nothing():
+    """An empty tensor has no address: the C call takes none with S_new = 0, checks the rest and returns."""
+    build.build()
+    lib = _lib.load()
+    p = 0x10000
+    pages, dims = _lib.Pages(9, 32, 4, p), _lib.Dims(B, Hkv, Hkv, d, 0.0)
+    empty = bf16(B, Hkv, 0, d)
+    assert empty.data_ptr() == 0
+    assert lib.e2d2_kv_cache_append_paged(p, p, pages, p, None, None, 0, p, p, p, dims, None) == 0
+    assert lib.e2d2_kv_cache_append_paged(p, p, pages, None, None, None, 0, p, p, p, dims, None) == 1
+    for k, v in ((None, p), (p, None)):
+        assert lib.e2d2_kv_cache_append_paged(p, p, pages, p, k, v, 1, p, p, p, dims, None) == 1

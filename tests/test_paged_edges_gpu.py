@@ -246,3 +246,14 @@ def test_an_eviction_makes_no_move_from_or_to_a_row_without_a_page(d, page, bad,
     three belong together before and after."""
     moved, error = run_evict([300, 290], 150, recent=10, d=d, page=page, bad=bad, in_place=in_place, seed=42)
     assert moved > 0 and error == E2D2_ERR_PAGE
+
+
+def test_an_append_of_no_rows():
+    k, w, pos = torch.ones(2, 3, 64, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(2, 3, 64, device="cuda"), \
+        torch.ones(2, 3, 64, dtype=torch.int32, device="cuda")
+    P = torch.zeros(2, dtype=torch.int32, device="cuda")
+    none = k[:, :, :0].contiguous()
+    v = k.clone()
+    attn.kv_cache_append_paged(k, v, None, P, none, none, weight=w, pos=pos, tokens=P)
+    torch.cuda.synchronize()
+    assert all((t == 1).all() for t in (k, v, w, pos)) and attn.last_device_error() == 0
