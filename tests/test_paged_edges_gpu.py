@@ -1,10 +1,12 @@
-"""GPU tests of the paged-cache calls at their edges: budgets of nothing, and what each call must leave alone.  Every
-buffer that a call may write lies inside a larger one whose margins are checked afterwards, the workspace too."""
+"""GPU tests of the paged-cache calls at their edges: budgets of nothing, values that are no numbers, pages that no pool
+holds, every shape of an eviction's launch, and what each call must leave alone.  Every buffer that a call may write lies
+inside a larger one whose margins are checked afterwards, the workspace too."""
 import numpy as np
 import pytest
 import torch
 
 from block_discrete_diffusion_tcgen05_b200 import attn
+import paged_reference as R
 
 pytestmark = pytest.mark.gpu
 
@@ -257,3 +259,149 @@ def test_an_append_of_no_rows():
     attn.kv_cache_append_paged(k, v, None, P, none, none, weight=w, pos=pos, tokens=P)
     torch.cuda.synchronize()
     assert all((t == 1).all() for t in (k, v, w, pos)) and attn.last_device_error() == 0
+
+
+# ------------------------------------------------------------- every shape of an eviction's launch
+def few_values(rng, shape):
+    """Many rows at the threshold, wherever it falls."""
+    return rng.choice(np.array([0.0, 0.25, 0.25, 0.25, 1.0, 3.0], np.float32), size=shape)
+
+
+LAUNCHES = [
+    # P, keep, recent, Hkv, capacity, d, page: blocks per head, threads of a block on 148 SMs
+    ([33000], 32500, 100, 80, 33000, 32, 48),          # 1, 1024: more rows than a block's shared memory has ranks for
+    ([33000], 16000, 0, 80, 33000, 32, 0),
+    ([5000], 2600, 64, 40, 5000, 64, 16),              # 2, 512
+    ([9000, 7], 4400, 10, 37, 9000, 32, 48),           # 2, 1024: a block on every SM
+    ([9000], 4400, 10, 40, 9000, 32, 48),              # 2, 1024
+    ([8192], 5000, 100, 1, 8192, 128, 64),             # 4, 512
+    ([8192, 100, 2100, 40], 30, 8, 5, 8200, 64, 16),   # 4, 512: short entries leave a cluster's later blocks without rows
+    ([20000, 33, 6000], 5000, 9, 7, 20000, 32, 128),   # 4, 1024
+    ([17000, 65], 8500, 0, 8, 17000, 32, 16),          # 8, 512
+    ([40000, 31], 20, 20, 4, 40000, 32, 0),            # 8, 1024
+]
+
+
+@pytest.mark.parametrize("P,keep,recent,Hkv,capacity,d,page", LAUNCHES)
+@pytest.mark.parametrize("weight", [few_values, None], ids=["ties", "distinct"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_every_launch_of_an_eviction(P, keep, recent, Hkv, capacity, d, page, weight, in_place):
+    """Clusters of 1, 2, 4 and 8 blocks of 512 and 1024 threads, ranks held in shared memory and read again, rows at the
+    threshold in every block of a cluster."""
+    moved, error = run_evict(P, keep, recent, d=d, page=page, Hkv=Hkv, capacity=capacity, weight=weight, in_place=in_place,
+                             dirty=True, seed=51)
+    assert moved > 0 and error == 0
+
+
+def test_equal_weights_keep_the_lowest_rows_across_a_cluster():
+    for Hkv, capacity in ((1, 8192), (40, 5000), (8, 17000)):
+        run_evict([capacity], capacity // 2 + 77, Hkv=Hkv, capacity=capacity, d=32, seed=52,
+                  weight=lambda rng, shape: np.full(shape, 0.5, np.float32))
+
+
+# ------------------------------------------------------------- pages that no pool holds, in every sampling kernel
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("page", [16, 48, 128])
+@pytest.mark.parametrize("rows", [1, 20, 64])
+@pytest.mark.parametrize("block", [False, True])
+def test_attention_leaves_out_rows_without_a_page(d, page, rows, block):
+    """A page in the middle, the one that the length ends in, and all of an entry's pages."""
+    each = 3 if page == 128 else 5
+    P = [each * page - 7, 2 * page, page + 1]
+    cache = R.Cache(3, 2, d, page, P, max(P), 5900 + page)
+    lost = [(0, 1), (0, each - 1), (2, 0), (2, 1)]
+    k, v, table, Pd = cache.cuda()
+    for i, (b, n) in enumerate(lost):
+        table[b, n] = (-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31)[i]
+    skip = {(b, r) for b, n in lost for r in range(n * page, min((n + 1) * page, P[b]))}
+    q = R.bf16((3, 2, rows, d), 5910)
+    kb, vb = (R.bf16((3, 2, rows, d), 5911), R.bf16((3, 2, rows, d), 5912)) if block else (None, None)
+    got = attn.decoder_sample_paged(q.cuda(), k, v, table, Pd, None if kb is None else kb.cuda(), None if vb is None else vb.cuda())
+    torch.cuda.synchronize()
+    assert attn.last_device_error() == E2D2_ERR_PAGE
+    R.check_sample(got, R.sample(cache, q, kb, vb, skip=skip), f"d{d} page{page} rows{rows}")
+    w = torch.rand(3, 2, cache.capacity, generator=torch.Generator().manual_seed(1))
+    ref, tol = R.weigh(cache, q, got[1].cpu(), w, skip=skip)
+    out = attn.kv_cache_weigh(q.cuda(), k, table, Pd, got[1], w.cuda())
+    torch.cuda.synchronize()
+    assert attn.last_device_error() == E2D2_ERR_PAGE
+    assert (np.abs(out.cpu().numpy() - ref) <= tol).all()
+
+
+# ------------------------------------------------------------- nothing outside the arguments is read
+@pytest.mark.parametrize("B,Hq,Hkv,S,d,page,block,P", [
+    (1, 1, 1, 1, 128, 0, True, [1]), (2, 6, 2, 5, 128, 16, True, [37, 200]), (1, 16, 2, 8, 128, 48, False, [141]),
+    (3, 4, 4, 7, 64, 0, False, [299, 1, 0]), (2, 8, 2, 16, 64, 80, True, [161, 80]), (1, 40, 2, 5, 32, 16, True, [333]),
+    (1, 2, 1, 33, 32, 0, True, [45])])
+def test_what_lies_around_the_arguments_is_not_read(B, Hq, Hkv, S, d, page, block, P):
+    """Every argument and the workspace between NaN: neither the attention nor the weights see it."""
+    cache = R.Cache(B, Hkv, d, page, P, max(P), 6000 + d, spare=0)
+    guard = Guarded(fill=0xFF)
+    k, v, table, Pd = (None if t is None else guard(t) for t in cache.cuda())
+    q = R.bf16((B, Hq, S, d), 6001)
+    kb, vb = (R.bf16((B, Hkv, S, d), 6002), R.bf16((B, Hkv, S, d), 6003)) if block else (None, None)
+    qd, kd, vd = (None if t is None else guard(t.cuda()) for t in (q, kb, vb))
+    ws = guard(attn.sample_paged_workspace(qd, k))
+    out, lse = guard(torch.zeros_like(qd)), guard(torch.zeros(B, Hq, S, device="cuda"))
+    attn.decoder_sample_paged(qd, k, v, table, Pd, kd, vd, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    R.check_sample((out, lse), R.sample(cache, q, kb, vb), "between NaN")
+    w = torch.rand(B, Hkv, cache.capacity, generator=torch.Generator().manual_seed(2))
+    ref, tol = R.weigh(cache, q, lse.cpu(), w)
+    wd, wo = guard(w.cuda()), guard(w.cuda())
+    attn.kv_cache_weigh(qd, k, table, Pd, lse, wd, out=wo)
+    torch.cuda.synchronize()
+    assert (np.abs(wo.cpu().numpy() - ref) <= tol).all()
+    guard.check()
+    assert attn.last_device_error() == 0
+
+
+# ------------------------------------------------------------- captured calls
+def test_captured_calls_with_a_workspace_zeroed_ahead_of_them():
+    """Two graphs with workspaces of their own, replayed at once on two streams; the warm-up waits for the zero-filling,
+    which runs on the stream of the allocation."""
+    cache = R.Cache(2, 4, 128, 16, [900, 333], 900, 7400)
+    k, v, table, P = cache.cuda()
+    made = []
+    for i in range(2):
+        q = R.bf16((2, 8, 1 + 3 * i, 128), 7401 + i)
+        qd = q.cuda()
+        ws = attn.sample_paged_workspace(qd, k)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            attn.decoder_sample_paged(qd, k, v, table, P, workspace=ws)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = attn.decoder_sample_paged(qd, k, v, table, P, workspace=ws)
+        made.append((g, torch.cuda.Stream(), out, R.sample(cache, q, None, None), ws, qd))
+    for _ in range(5):
+        for g, s, *_ in made:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, out, ref, *_ in made:
+        R.check_sample(out, ref, "captured")
+    assert attn.last_device_error() == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,S,d,page,lo,hi", [(1, 16, 8, 1, 128, 64, 500, 500), (8, 16, 8, 16, 128, 64, 2048, 2048),
+                                                     (2, 32, 8, 16, 128, 128, 7000, 8192), (5, 12, 4, 7, 64, 48, 1, 3001)])
+def test_repeated_calls_give_the_same_bits(B, Hq, Hkv, S, d, page, lo, hi):
+    """Units shared by several blocks are joined in the blocks' order, whichever finishes last."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(61)
+    normal = lambda *shape: torch.randn(shape, device="cuda", generator=g).bfloat16()  # noqa: E731
+    each = -(-hi // page)
+    k, v = normal(B * each, Hkv, page, d), normal(B * each, Hkv, page, d)
+    table = torch.randperm(B * each, device="cuda", generator=g).view(B, each).int().contiguous()
+    P = torch.linspace(lo, hi, B, device="cuda").int()
+    q, kb, vb = normal(B, Hq, S, d), normal(B, Hkv, S, d), normal(B, Hkv, S, d)
+    ws = attn.sample_paged_workspace(q, k)
+    first = attn.decoder_sample_paged(q, k, v, table, P, kb, vb, workspace=ws)
+    for _ in range(30):
+        again = attn.decoder_sample_paged(q, k, v, table, P, kb, vb, workspace=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert attn.last_device_error() == 0
