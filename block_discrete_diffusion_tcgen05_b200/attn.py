@@ -570,7 +570,7 @@ def kv_cache_evict(k_pages, v_pages, page_table, P, weight, pos, tokens, keep: i
 
 def last_device_error(device=None) -> int:
     lib = _lib.load()
-    return int(lib.e2d2_last_device_error(torch.cuda.current_stream(device).cuda_stream))
+    return int(lib.e2d2_last_device_error(ctypes_stream(torch.cuda.current_stream(device))))
 
 
 def default_scale(head_dim: int) -> float:

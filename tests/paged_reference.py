@@ -60,7 +60,7 @@ class Cache:
         return torch.stack([t[pg, h, i] for pg, i in (self.where(b, r) for r in range(n))])
 
     def cuda(self):
-        """(k, v, table, P) on the GPU; the pools sit between NaN guard bands."""
+        """(k, v, table, P) on the GPU."""
         return (self.k.cuda(), self.v.cuda(), None if self.table is None else self.table.cuda(),
                 torch.tensor(self.P, dtype=torch.int32, device="cuda"))
 
