@@ -2,12 +2,13 @@
 
     python -m block_discrete_diffusion_tcgen05_b200.ncu_case \
         {encoder|decoder_train|encoder_backward|decoder_backward|decoder_sample|kv_append|
-         paged_token|paged_block|append_paged|weigh|evict} [repeats]
+         paged_token|paged_block|paged_wide|paged_d64|append_paged|weigh|evict|evict_prompt} [repeats]
 
 Shapes are the benchmark's: E2D2 train pass (B8 L1024 S16 H16 d64) for the two train calls and
 their backward (one forward call, then `repeats` backward calls),
 E2D2 sampling step (B32 P2048 S16 Hq16 Hkv8 d128) for the sampling call and the append, and the same over
-pages of 64 rows for the paged calls (paged_token: S1; evict: to half of the rows).
+pages of 64 rows for the paged calls (paged_token: S1; evict: to half of the rows; paged_wide and evict_prompt:
+B4 P32768 Hq32 Hkv8, to a quarter of the rows; paged_d64: B4 P6000 Hq32 Hkv8 d64).
 Inputs are seeded normals drawn on the device (the values do not change the work)."""
 from __future__ import annotations
 
@@ -62,13 +63,15 @@ def main(argv):
                 attn.decoder_sample(q, kc, vc, sw.P, kb, vb, workspace=ws)
             else:
                 attn.kv_cache_append(kc, vc, sw.P, kb, vb)
-    elif which in ("paged_token", "paged_block", "append_paged", "weigh", "evict"):
-        B, Hq, Hkv, d, page = sw.batch, sw.q_heads, sw.kv_heads, sw.head_dim, 64
-        S = 1 if which == "paged_token" else sw.S
-        each = -(-(sw.P + sw.S) // page)
+    elif which in ("paged_token", "paged_block", "paged_wide", "paged_d64", "append_paged", "weigh", "evict", "evict_prompt"):
+        long = {"paged_wide": (4, 32, 8, 128, 32768), "paged_d64": (4, 32, 8, 64, 6000), "evict_prompt": (4, 8, 8, 128, 32768)}
+        B, Hq, Hkv, d, rows = long.get(which, (sw.batch, sw.q_heads, sw.kv_heads, sw.head_dim, sw.P))
+        S, page = 1 if which == "paged_token" else sw.S, 64
+        keep = rows // (4 if which == "evict_prompt" else 2)
+        each = -(-(rows + S) // page)
         kp, vp = (rnd(B * each, Hkv, page, d) for _ in range(2))
         table = torch.randperm(B * each, generator=g, device=dev).view(B, each).to(torch.int32)
-        P = torch.full((B,), sw.P, dtype=torch.int32, device=dev)
+        P = torch.full((B,), rows, dtype=torch.int32, device=dev)
         q = rnd(B, Hq, S, d)
         kb, vb = (rnd(B, Hkv, S, d) for _ in range(2))
         w = torch.rand(B, Hkv, each * page, generator=g, device=dev)
@@ -77,14 +80,14 @@ def main(argv):
         w_out, pos_out, P_out = torch.zeros_like(w), torch.zeros_like(pos), torch.zeros_like(P)
         lse = attn.decoder_sample_paged(q, kp, vp, table, P, workspace=ws)[1]
         for _ in range(reps):
-            if which in ("paged_token", "paged_block"):
+            if which.startswith("paged_"):
                 attn.decoder_sample_paged(q, kp, vp, table, P, kb, vb, workspace=ws)
             elif which == "append_paged":
                 attn.kv_cache_append_paged(kp, vp, table, P, kb, vb)
             elif which == "weigh":
                 attn.kv_cache_weigh(q, kp, table, P, lse, w, out=w_out)
             else:
-                attn.kv_cache_evict(kp, vp, table, P, w, pos, P, sw.P // 2, recent=64, weight_out=w_out, pos_out=pos_out,
+                attn.kv_cache_evict(kp, vp, table, P, w, pos, P, keep, recent=64, weight_out=w_out, pos_out=pos_out,
                                     P_out=P_out, workspace=ews)
     else:
         raise SystemExit(f"unknown call {which}")
