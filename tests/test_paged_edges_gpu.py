@@ -405,3 +405,21 @@ def test_repeated_calls_give_the_same_bits(B, Hq, Hkv, S, d, page, lo, hi):
         again = attn.decoder_sample_paged(q, k, v, table, P, kb, vb, workspace=ws)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     assert attn.last_device_error() == 0
+
+
+def test_one_workspace_serves_attention_of_other_shapes():
+    """Zero-filled once, then calls of other head sizes, rows, batches and lengths on the same stream."""
+    shapes = [(2, 16, 2, 8, 128, 16, [900, 333]), (1, 2, 1, 1, 64, 48, [1500]), (3, 8, 2, 16, 128, 64, [700, 0, 129]),
+              (2, 4, 4, 7, 32, 16, [299, 800]), (1, 8, 8, 1, 128, 32, [2100])]
+    made, ws = [], torch.zeros(max(attn.sample_paged_workspace_bytes(B, Hq, Hkv, d, S) for B, Hq, Hkv, S, d, _, _ in shapes),
+                               dtype=torch.uint8, device="cuda")
+    for i, (B, Hq, Hkv, S, d, page, P) in enumerate(shapes):
+        cache = R.Cache(B, Hkv, d, page, P, max(P), 6200 + i)
+        q = R.bf16((B, Hq, S, d), 6210 + i)
+        made.append((q.cuda(), *cache.cuda(), R.sample(cache, q, None, None)))
+    for _ in range(2):
+        got = [attn.decoder_sample_paged(q, k, v, table, P, workspace=ws) for q, k, v, table, P, _ in made]
+        torch.cuda.synchronize()
+        for g, m in zip(got, made):
+            R.check_sample(g, m[-1], "one workspace")
+    assert attn.last_device_error() == 0
