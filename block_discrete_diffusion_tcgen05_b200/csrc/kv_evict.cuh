@@ -1,11 +1,11 @@
 // kv_evict.cuh -- eviction from a KV cache by accumulated attention weight.
 //
 // Per (entry, kv head): of the P rows, `keep` stay.  Rows at positions >= tokens - recent come first, then
-// the rows by decreasing weight, ties to the lowest row.  Kept rows below `keep` stay where they are; the
-// i-th kept row at or past `keep` (a mover) goes to the i-th row below `keep` that is not kept (a hole), so
-// a call moves no more rows than it must, and sources (at or past keep) and targets (below it) never
-// overlap.  Attention over the prefix does not depend on the order of its rows; pos says which token each
-// one is.
+// the rows by decreasing weight, ties to the lowest row (keep = 0: none, and nothing moves).  Kept rows below
+// `keep` stay where they are; the i-th kept row at or past `keep` (a mover) goes to the i-th row below `keep`
+// that is not kept (a hole), so a call moves no more rows than it must, and sources (at or past keep) and
+// targets (below it) never overlap.  Attention over the prefix does not depend on the order of its rows; pos
+// says which token each one is.
 //
 // One launch: a cluster of 1 to 8 blocks per (entry, kv head), each with a slice of the rows.  It reads 8 bytes a row
 // once, keeps the slice's ranks in shared memory (up to 32768 rows), and finds the keep-th largest by 11, 11 and 10
@@ -15,8 +15,8 @@
 // it: no sort, and no order that depends on timing.  The cluster's warps then move the rows, K and V, eight at a time.
 // The new lengths may lie where the old ones do: the last cluster to have read its own writes them all.
 //
-// 256 heads of 2064 rows, 16 moves each: 10.5 us, bound by a dozen block-wide steps.  32 heads of 32768 rows to 8192 on
-// clusters of four: 56.8 us, of which about 19 find the rows and 38 move 198 MB in rows of 256 bytes (5.2 TB/s); half
+// 256 heads of 2064 rows, 16 moves each: 10.9 us, bound by a dozen block-wide steps.  32 heads of 32768 rows to 8192 on
+// clusters of four: 56 us, of which about 19 find the rows and 38 move 198 MB in rows of 256 bytes (5.2 TB/s); half
 // the warps moving: 71 us.  Two launches, the second moving the rows from the whole GPU, took 14.8 and 62 us, 2 to 3 us
 // more outside a graph, and were faster only where few heads leave SMs idle (8 heads of 32768 rows: 40.6 against 43.5).
 // 64 registers, so that 512-thread blocks share an SM in pairs: 22 us for the 256 heads without.

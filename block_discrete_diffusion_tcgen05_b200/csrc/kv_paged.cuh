@@ -176,7 +176,7 @@ struct PagedAppendParams {
 };
 
 // A pure copy, HBM-bound: a warp per eight new rows, grid-stride.  4 prompts of 4095 tokens (135 MB read and written)
-// take 26.6 us, 5.1 TB/s; one 16-byte vector per thread and step, with its row looked up by every thread, took 44 us.
+// take 26.3 us, 5.1 TB/s; one 16-byte vector per thread and step, with its row looked up by every thread, took 44 us.
 // Four blocks per SM: five spill (32 us).
 template <int VPR>
 __global__ void __launch_bounds__(256, 4) kv_append_paged_kernel(const __grid_constant__ PagedAppendParams a) {

@@ -7,11 +7,11 @@
 //
 // P and R are the two bf16 that hold a probability to 16 bits and more: the remainders are N more columns of the same
 // product, added to the others' when the unit ends.  A tile's softmax is that of 128 threads for every 16 columns
-// (thread = key) and the tensor cores work beside it.  HBM bounds it: 32 single tokens over up to 8192 rows take 93 us
-// (5.7 TB/s, 87 % of the copy rate), 32 blocks of 16 tokens over 2048 rows with 32 query rows per head 50 us
-// (5.5 TB/s); with 64 query rows (4 blocks over 32768 rows: 105 us, 5.0 TB/s) the softmax's 64 columns come close to
-// HBM's pace, and follow the SM's clock: 116 us once a stretch of such calls has drawn it down.  Short calls are a chain
-// of latencies: one token over 500 rows takes 9.2 us.
+// (thread = key) and the tensor cores work beside it.  HBM bounds it up to 32 query rows per head: 32 single tokens over up
+// to 8192 rows take 93 us (5.7 TB/s, 87 % of the copy rate), 32 blocks of 16 tokens over 2048 rows with 32 query rows 51 us
+// (5.4 TB/s).  With 64 (4 blocks over up to 32768 rows) the softmax's chain of waits per tile does, and follows the SM's
+// clock: 118 us, 4.4 TB/s, as calls one after the other, 103 us in stretches too short to draw the clock down.  Short
+// calls are a chain of latencies: one token over 500 rows takes 9.3 us.
 //
 // A column's running maximum is shared by its warpgroup's 128 keys: each tile the threads vote whether any key beats
 // any of their columns' by more than 2^8, and only then are they reduced and O^T rescaled.  It is held negated and in
